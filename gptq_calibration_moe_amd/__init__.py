@@ -26,6 +26,8 @@ STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "SHAPE", 3: "ALIGN", 4: "HIP", 5: 
 ALPHA_MODES = {"rt": 0, "eq": 1, "explicit": 2, "explicit_slot": 3}
 F32, BF16 = 0, 1
 GPTQ_ACT_ORDER, GPTQ_STATIC_GROUPS = 1, 2   # clha_gptq_flag
+SCORES = {"softmax": 0, "sigmoid": 1}        # clha_score
+GROUP_SCORES = {"max": 0, "top2": 1}         # clha_group_score
 
 EXPORTS = (
     "clha_create", "clha_destroy", "clha_last_error", "clha_num_slots", "clha_register_layer",
@@ -36,8 +38,11 @@ EXPORTS = (
     "clha_inverse_cholesky", "clha_loss_workspace_bytes", "clha_loss", "clha_set_timing",
     "clha_read_timing", "clha_sync", "clha_pack_codes", "clha_unpack_codes",
     "clha_down_workspace_bytes", "clha_collect_down_hessians", "clha_loss_static",
+    "clha_route", "clha_collect_hessians_scored", "clha_mx_quantize", "clha_mx_dequantize", "clha_mx_matmul",
+    "clha_mx_experts_workspace_bytes", "clha_mx_experts",
 )
-STAGES = ("route", "bucket", "gather", "syrk", "aggregate", "factor", "gptq", "loss", "syrk_reduce")
+STAGES = ("route", "bucket", "gather", "syrk", "aggregate", "factor", "gptq", "loss", "syrk_reduce",
+          "mx_quantize", "mx_matmul", "mx_experts")
 
 
 class ClhaError(RuntimeError):
@@ -57,6 +62,21 @@ class GptqJob(C.Structure):
                 ("scales", C.c_void_p), ("zeros", C.c_void_p), ("loss", C.c_void_p),
                 ("H_eval", C.c_void_p), ("loss_eval", C.c_void_p), ("dead", C.c_void_p),
                 ("status", C.c_void_p)]
+
+
+class RouteDesc(C.Structure):
+    _fields_ = [("score", C.c_int32), ("n_groups", C.c_int32), ("top_groups", C.c_int32),
+                ("group_score", C.c_int32), ("renormalize", C.c_int32), ("scale", C.c_float)]
+
+
+def route_desc(score: str = "softmax", groups: int = 1, top_groups: int = 1, group_score: str = "max",
+               renormalize: bool = True, scale: float = 1.0) -> RouteDesc:
+    """How tokens choose experts by scores (clha_route_desc)."""
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    if group_score not in GROUP_SCORES:
+        raise ValueError(f"group_score must be one of {sorted(GROUP_SCORES)}, got {group_score!r}")
+    return RouteDesc(SCORES[score], groups, top_groups, GROUP_SCORES[group_score], 1 if renormalize else 0, scale)
 
 
 def _load() -> C.CDLL:
@@ -92,6 +112,14 @@ def _load() -> C.CDLL:
         "clha_set_timing": ([vp, i32], i32),
         "clha_read_timing": ([vp, C.POINTER(C.c_double), C.POINTER(i64), i32], i32),
         "clha_sync": ([vp, vp], i32),
+        "clha_route": ([vp, C.POINTER(RouteDesc), i64, vp, vp, vp, vp, vp], i32),
+        "clha_collect_hessians_scored": ([vp, i32, C.POINTER(RouteDesc), i64, vp, vp, vp, vp, vp, vp, vp, vp, sz,
+                                          vp], i32),
+        "clha_mx_quantize": ([vp, i64, i32, vp, i32, i64, vp, vp, vp], i32),
+        "clha_mx_dequantize": ([vp, i64, i32, vp, vp, vp, i32, vp], i32),
+        "clha_mx_matmul": ([vp, i64, i32, i32, vp, vp, vp, vp, vp, i32, vp], i32),
+        "clha_mx_experts_workspace_bytes": ([vp, i64, i32], sz),
+        "clha_mx_experts": ([vp, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -253,8 +281,14 @@ class Context:
                          topk_out: Optional[torch.Tensor] = None,
                          offsets_out: Optional[torch.Tensor] = None,
                          token_ids_out: Optional[torch.Tensor] = None,
-                         workspace: Optional[torch.Tensor] = None, stream=None):
+                         workspace: Optional[torch.Tensor] = None, stream=None,
+                         routing: Optional[RouteDesc] = None, bias: Optional[torch.Tensor] = None,
+                         weights_out: Optional[torch.Tensor] = None):
+        """routing (route_desc(...)) selects clha_collect_hessians_scored: the block's own choice of
+        experts by scores, with an optional bias [E] and the chosen weights out."""
         n = x.shape[0]
+        if routing is None and (bias is not None or weights_out is not None):
+            raise ValueError("bias and weights_out need a routing by scores")
         _check_dev("x", x, (torch.bfloat16, torch.int16, torch.uint16), (n, self.d), self.device)
         _check_dev("logits", logits, torch.float32, (n, self.n_routed), self.device)
         if topk_out is not None:
@@ -265,6 +299,15 @@ class Context:
             _check_dev("token_ids_out", token_ids_out, torch.int32, (n * self.top_k,), self.device)
         need = self.collect_workspace_bytes()
         ws = workspace if workspace is not None else self.workspace("collect", need)
+        if routing is not None:
+            if bias is not None:
+                _check_dev("bias", bias, torch.float32, (self.n_routed,), self.device)
+            if weights_out is not None:
+                _check_dev("weights_out", weights_out, torch.float32, (n, self.top_k), self.device)
+            self._raise(lib.clha_collect_hessians_scored(
+                self._h, layer, C.byref(routing), n, _ptr(_bits16(x)), _ptr(logits), _ptr(bias), _ptr(topk_out),
+                _ptr(weights_out), _ptr(offsets_out), _ptr(token_ids_out), _ptr(ws), ws.numel(), _stream(stream)))
+            return
         self._raise(lib.clha_collect_hessians(
             self._h, layer, n, _ptr(_bits16(x)), _ptr(logits), _ptr(topk_out), _ptr(offsets_out),
             _ptr(token_ids_out), _ptr(ws), ws.numel(), _stream(stream)))
@@ -432,6 +475,139 @@ class Context:
                                          BF16 if W.dtype == torch.bfloat16 else F32, _ptr(codes),
                                          _ptr(scales), _ptr(zeros), _ptr(H), _ptr(loss_out),
                                          _stream(stream)))
+
+    # ------------------------------------------------------------------ routing by scores, MXFP4
+    # These calls run on `stream`, or on the current stream of the context's device; outputs and
+    # workspaces that they make belong to that stream.
+
+    def _on(self, stream):
+        return torch.cuda.current_stream(self.device) if stream is None else stream
+
+    def _new(self, shape, dtype, stream):
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def route(self, logits: torch.Tensor, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+              groups: int = 1, top_groups: int = 1, group_score: str = "max", renormalize: bool = True,
+              scale: float = 1.0, topk_out: Optional[torch.Tensor] = None,
+              weights_out: Optional[torch.Tensor] = None, stream=None):
+        """clha_route: (topk int32 [n, K], weights float32 [n, K]) of logits [n, E]."""
+        n = logits.shape[0]
+        _check_dev("logits", logits, torch.float32, (n, self.n_routed), self.device)
+        if bias is not None:
+            _check_dev("bias", bias, torch.float32, (self.n_routed,), self.device)
+        desc = route_desc(score, groups, top_groups, group_score, renormalize, scale)
+        topk = self._new((n, self.top_k), torch.int32, stream) if topk_out is None else topk_out
+        weights = self._new((n, self.top_k), torch.float32, stream) if weights_out is None else weights_out
+        if topk_out is not None:
+            _check_dev("topk_out", topk, torch.int32, (n, self.top_k), self.device)
+        if weights_out is not None:
+            _check_dev("weights_out", weights, torch.float32, (n, self.top_k), self.device)
+        self._raise(lib.clha_route(self._h, C.byref(desc), n, _ptr(logits), _ptr(bias), _ptr(topk), _ptr(weights),
+                                   _stream(self._on(stream))))
+        return topk, weights
+
+    def mx_quantize(self, x: torch.Tensor, codes_out: Optional[torch.Tensor] = None,
+                    scales_out: Optional[torch.Tensor] = None, stream=None):
+        """clha_mx_quantize: (codes uint8 [..., cols/2], scales uint8 [..., cols/32]) of a contiguous
+        fp32 or bf16 tensor, or of a matrix whose rows are contiguous."""
+        cols = x.shape[-1]
+        rows = x.numel() // cols if cols else 0
+        ld = cols
+        if x.dim() == 2 and x.stride(1) == 1 and rows > 1:
+            ld = x.stride(0)
+            _check_dev("x", x[0], (torch.float32, torch.bfloat16), None, self.device)
+        else:
+            _check_dev("x", x, (torch.float32, torch.bfloat16), None, self.device)
+        if cols % 32:
+            raise ValueError("the last dimension of x must be a multiple of 32")
+        shape, sshape = (*x.shape[:-1], cols // 2), (*x.shape[:-1], cols // 32)
+        codes = self._new(shape, torch.uint8, stream) if codes_out is None else codes_out
+        scales = self._new(sshape, torch.uint8, stream) if scales_out is None else scales_out
+        if codes_out is not None:
+            _check_dev("codes_out", codes, torch.uint8, shape, self.device)
+        if scales_out is not None:
+            _check_dev("scales_out", scales, torch.uint8, sshape, self.device)
+        self._raise(lib.clha_mx_quantize(self._h, rows, cols, _ptr(x), BF16 if x.dtype == torch.bfloat16 else F32,
+                                         ld, _ptr(codes), _ptr(scales), _stream(self._on(stream))))
+        return codes, scales
+
+    def _check_mx(self, name, codes, scales):
+        _check_dev(name, codes, torch.uint8, None, self.device)
+        if codes.dim() < 1 or codes.shape[-1] % 16:
+            raise ValueError(f"{name} needs rows of a multiple of 32 values (16 bytes)")
+        _check_dev(name + "_scales", scales, torch.uint8, (*codes.shape[:-1], codes.shape[-1] // 16), self.device)
+
+    def mx_dequantize(self, codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """clha_mx_dequantize: the values [..., cols] in fp32 or bf16."""
+        self._check_mx("codes", codes, scales)
+        cols = 2 * codes.shape[-1]
+        shape = (*codes.shape[:-1], cols)
+        dt = self._out_type(dtype)
+        y = self._new(shape, dtype, stream) if out is None else out
+        if out is not None:
+            _check_dev("out", y, dtype, shape, self.device)
+        self._raise(lib.clha_mx_dequantize(self._h, codes.numel() // (cols // 2) if cols else 0, cols, _ptr(codes),
+                                           _ptr(scales), _ptr(y), dt, _stream(self._on(stream))))
+        return y
+
+    @staticmethod
+    def _out_type(dtype):
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"results are bfloat16 or float32, not {dtype}")
+        return BF16 if dtype == torch.bfloat16 else F32
+
+    def mx_matmul(self, a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                  dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+        """clha_mx_matmul: a [m, k] times w [n, k] transposed, both MXFP4, in fp32 or bf16 [m, n]."""
+        self._check_mx("a", a, a_scales)
+        self._check_mx("w", w, w_scales)
+        if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
+            raise ValueError(f"a {tuple(a.shape)} and w {tuple(w.shape)} must be matrices of equal row length")
+        m, n, k = a.shape[0], w.shape[0], 2 * a.shape[1]
+        dt = self._out_type(dtype)
+        y = self._new((m, n), dtype, stream) if out is None else out
+        if out is not None:
+            _check_dev("out", y, dtype, (m, n), self.device)
+        self._raise(lib.clha_mx_matmul(self._h, m, n, k, _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(y),
+                                       dt, _stream(self._on(stream))))
+        return y
+
+    def mx_experts_workspace_bytes(self, n_tokens: int, f: int) -> int:
+        return lib.clha_mx_experts_workspace_bytes(self._h, n_tokens, f)
+
+    def mx_experts(self, x: torch.Tensor, topk: torch.Tensor, weights: torch.Tensor, wgu: torch.Tensor,
+                   wgu_scales: torch.Tensor, wd: torch.Tensor, wd_scales: torch.Tensor,
+                   dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """clha_mx_experts: x [n, d] bf16 through the block's MXFP4 experts, E routed ones chosen by
+        (topk, weights) [n, K] and the shared ones; wgu [E + n_shared, 2f, d], wd [E + n_shared, d, f]."""
+        n, d, experts = x.shape[0], self.d, self.n_routed + self.n_shared
+        f = 2 * wd.shape[-1]
+        _check_dev("x", x, (torch.bfloat16, torch.int16, torch.uint16), (n, d), self.device)
+        _check_dev("topk", topk, torch.int32, (n, self.top_k), self.device)
+        _check_dev("weights", weights, torch.float32, (n, self.top_k), self.device)
+        _check_dev("wgu", wgu, torch.uint8, (experts, 2 * f, d // 2), self.device)
+        _check_dev("wgu_scales", wgu_scales, torch.uint8, (experts, 2 * f, d // 32), self.device)
+        _check_dev("wd", wd, torch.uint8, (experts, d, f // 2), self.device)
+        _check_dev("wd_scales", wd_scales, torch.uint8, (experts, d, f // 32), self.device)
+        dt = self._out_type(dtype)
+        y = self._new((n, d), dtype, stream) if out is None else out
+        if out is not None:
+            _check_dev("out", y, dtype, (n, d), self.device)
+        ws = workspace
+        if ws is None:
+            ws = self._new((max(self.mx_experts_workspace_bytes(n, f), 256),), torch.uint8, stream)
+        else:
+            _check_dev("workspace", ws, torch.uint8, None, self.device)
+        self._raise(lib.clha_mx_experts(self._h, n, f, _ptr(x), _ptr(topk), _ptr(weights), _ptr(wgu),
+                                        _ptr(wgu_scales), _ptr(wd), _ptr(wd_scales), _ptr(y), dt, _ptr(ws),
+                                        ws.numel(), _stream(self._on(stream))))
+        return y
 
     def set_timing(self, enable: bool):
         self._raise(lib.clha_set_timing(self._h, 1 if enable else 0))

@@ -18,6 +18,7 @@
 
 using clha::AggArgs;
 using clha::CollectPlan;
+using clha::ExpertsPlan;
 using clha::GJob;
 using clha::GptqPlan;
 
@@ -123,6 +124,19 @@ struct StageTimer {
     }
     hipEventRecord(b, s);
     ctx->recs.push_back({stage, a, b});
+  }
+};
+
+// Makes the context's device current for one call: a launch goes to the current
+// device, whichever device the caller has selected.
+struct OnDevice {
+  int before = -1, want;
+  explicit OnDevice(const clha_ctx* c) : want(c->device) {
+    if (hipGetDevice(&before) != hipSuccess) before = -1;
+    if (before != want) hipSetDevice(want);
+  }
+  ~OnDevice() {
+    if (before >= 0 && before != want) hipSetDevice(before);
   }
 };
 
@@ -448,28 +462,62 @@ CLHA_API size_t clha_collect_workspace_bytes(const clha_ctx* ctx) {
   return collect_layout(ctx, nullptr).bytes;
 }
 
-CLHA_API clha_status clha_collect_hessians(clha_ctx* ctx, int32_t layer, int64_t n_tokens,
-                                           const uint16_t* x, const float* logits,
-                                           int32_t* topk_out, int64_t* offsets_out,
-                                           int32_t* token_ids_out, void* workspace,
-                                           size_t workspace_bytes, void* stream) {
+// Routing of a collection or of clha_route: null desc is the K largest logits.
+struct Scored {
+  const clha_route_desc* desc = nullptr;
+  const float* bias = nullptr;
+  float* weights_out = nullptr;
+};
+
+static clha::RouteArgs route_args(const clha_route_desc& d) {
+  return clha::RouteArgs{d.score, d.n_groups, d.top_groups, d.group_score, d.renormalize, d.scale};
+}
+
+static clha_status check_route(clha_ctx* ctx, const char* what, const clha_route_desc* d, int64_t n_tokens) {
+  if (!d) return fail(ctx, CLHA_ERR_INVALID_ARG, "%s: null description", what);
+  const int E = ctx->desc.n_routed, K = ctx->desc.top_k;
+  if (d->score != CLHA_SCORE_SOFTMAX && d->score != CLHA_SCORE_SIGMOID)
+    return fail(ctx, CLHA_ERR_INVALID_ARG, "%s: unknown score %d", what, d->score);
+  if (!std::isfinite(d->scale)) return fail(ctx, CLHA_ERR_INVALID_ARG, "%s: scale must be finite", what);
+  if (d->renormalize != 0 && d->renormalize != 1)
+    return fail(ctx, CLHA_ERR_INVALID_ARG, "%s: renormalize must be 0 or 1", what);
+  if (d->n_groups < 1 || E % d->n_groups != 0)
+    return fail(ctx, CLHA_ERR_SHAPE, "%s: %d groups do not divide %d experts", what, d->n_groups, E);
+  if (d->top_groups < 1 || d->top_groups > d->n_groups)
+    return fail(ctx, CLHA_ERR_SHAPE, "%s: top_groups %d outside 1..%d", what, d->top_groups, d->n_groups);
+  if (d->n_groups > 1 && d->group_score != CLHA_GROUP_MAX && d->group_score != CLHA_GROUP_TOP2)
+    return fail(ctx, CLHA_ERR_INVALID_ARG, "%s: unknown group score %d", what, d->group_score);
+  if (K > d->top_groups * (E / d->n_groups))
+    return fail(ctx, CLHA_ERR_SHAPE, "%s: %d groups of %d experts hold fewer than %d", what, d->top_groups,
+                E / d->n_groups, K);
+  if (n_tokens < 0 || n_tokens > clha::kMaxRouteTokens)
+    return fail(ctx, CLHA_ERR_SHAPE, "%s: n_tokens %lld outside 0..%lld", what, (long long)n_tokens,
+                (long long)clha::kMaxRouteTokens);
+  return CLHA_OK;
+}
+
+// Both forms of the collection; messages name the entry point `what`.
+static clha_status collect(clha_ctx* ctx, const char* what, const Scored& sc, int32_t layer, int64_t n_tokens,
+                           const uint16_t* x, const float* logits, int32_t* topk_out, int64_t* offsets_out,
+                           int32_t* token_ids_out, void* workspace, size_t workspace_bytes, void* stream) {
   if (!ctx) return CLHA_ERR_INVALID_ARG;
   auto it = ctx->layers.find(layer);
   if (it == ctx->layers.end())
-    return fail(ctx, CLHA_ERR_INVALID_ARG, "collect_hessians: layer %d is not registered", layer);
+    return fail(ctx, CLHA_ERR_INVALID_ARG, "%s: layer %d is not registered", what, layer);
   if (n_tokens < 0 || n_tokens > ctx->desc.max_tokens)
-    return fail(ctx, CLHA_ERR_SHAPE, "collect_hessians: n_tokens %lld outside 0..%lld",
+    return fail(ctx, CLHA_ERR_SHAPE, "%s: n_tokens %lld outside 0..%lld", what,
                 (long long)n_tokens, (long long)ctx->desc.max_tokens);
   if (n_tokens == 0) return CLHA_OK;   // an empty batch adds nothing; its pointers are not read
   if (!x || !logits || !workspace)
-    return fail(ctx, CLHA_ERR_INVALID_ARG, "collect_hessians: null x, logits or workspace");
+    return fail(ctx, CLHA_ERR_INVALID_ARG, "%s: null x, logits or workspace", what);
   if (!aligned16(x) || !aligned4(logits) || !aligned16(workspace) ||
-      (topk_out && !aligned4(topk_out)) || (offsets_out && !aligned16(offsets_out)) ||
+      (topk_out && !aligned4(topk_out)) || (sc.bias && !aligned4(sc.bias)) ||
+      (sc.weights_out && !aligned4(sc.weights_out)) || (offsets_out && !aligned16(offsets_out)) ||
       (token_ids_out && !aligned4(token_ids_out)))
-    return fail(ctx, CLHA_ERR_ALIGN, "collect_hessians: misaligned pointer");
+    return fail(ctx, CLHA_ERR_ALIGN, "%s: misaligned pointer", what);
   const CollectLayout need = collect_layout(ctx, nullptr);
   if (workspace_bytes < need.bytes)
-    return fail(ctx, CLHA_ERR_WORKSPACE, "collect_hessians: workspace %zu < %zu bytes",
+    return fail(ctx, CLHA_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", what,
                 workspace_bytes, need.bytes);
   const CollectLayout L = collect_layout(ctx, workspace);
   const clha_moe_desc& d = ctx->desc;
@@ -509,7 +557,11 @@ CLHA_API clha_status clha_collect_hessians(clha_ctx* ctx, int32_t layer, int64_t
   const hipStream_t s = as_stream(stream);
   {
     StageTimer t(ctx, CLHA_STAGE_ROUTE, s);
-    clha::launch_route(logits, p, s);
+    if (sc.desc)
+      clha::launch_score_route(logits, sc.bias, n_tokens, p.E, p.K, route_args(*sc.desc), p.topk, sc.weights_out,
+                               p.iota, p.status, layer, true, s);
+    else
+      clha::launch_route(logits, p, s);
   }
   {
     StageTimer t(ctx, CLHA_STAGE_BUCKET, s);
@@ -524,7 +576,44 @@ CLHA_API clha_status clha_collect_hessians(clha_ctx* ctx, int32_t layer, int64_t
     clha::launch_syrk_reduce(p, it->second.S, it->second.counts, s);
   }
   it->second.fresh = false;
-  return hip_check(ctx, "collect_hessians");
+  return hip_check(ctx, what);
+}
+
+CLHA_API clha_status clha_collect_hessians(clha_ctx* ctx, int32_t layer, int64_t n_tokens,
+                                           const uint16_t* x, const float* logits,
+                                           int32_t* topk_out, int64_t* offsets_out,
+                                           int32_t* token_ids_out, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  if (!ctx) return CLHA_ERR_INVALID_ARG;
+  return collect(ctx, "collect_hessians", Scored{}, layer, n_tokens, x, logits, topk_out, offsets_out, token_ids_out,
+                 workspace, workspace_bytes, stream);
+}
+
+CLHA_API clha_status clha_collect_hessians_scored(clha_ctx* ctx, int32_t layer, const clha_route_desc* desc,
+                                                  int64_t n_tokens, const uint16_t* x, const float* logits,
+                                                  const float* bias, int32_t* topk_out, float* weights_out,
+                                                  int64_t* offsets_out, int32_t* token_ids_out, void* workspace,
+                                                  size_t workspace_bytes, void* stream) {
+  if (!ctx) return CLHA_ERR_INVALID_ARG;
+  const clha_status st = check_route(ctx, "collect_hessians_scored", desc, n_tokens);
+  if (st != CLHA_OK) return st;
+  return collect(ctx, "collect_hessians_scored", Scored{desc, bias, weights_out}, layer, n_tokens, x, logits, topk_out,
+                 offsets_out, token_ids_out, workspace, workspace_bytes, stream);
+}
+
+CLHA_API clha_status clha_route(clha_ctx* ctx, const clha_route_desc* desc, int64_t n_tokens, const float* logits,
+                                const float* bias, int32_t* topk_out, float* weights_out, void* stream) {
+  if (!ctx) return CLHA_ERR_INVALID_ARG;
+  const clha_status st = check_route(ctx, "route", desc, n_tokens);
+  if (st != CLHA_OK || n_tokens == 0) return st;
+  if (!logits || !topk_out) return fail(ctx, CLHA_ERR_INVALID_ARG, "route: null logits or topk_out");
+  if (!aligned4(logits) || !aligned4(bias) || !aligned4(topk_out) || !aligned4(weights_out))
+    return fail(ctx, CLHA_ERR_ALIGN, "route: misaligned pointer");
+  const OnDevice on(ctx);
+  StageTimer t(ctx, CLHA_STAGE_ROUTE, as_stream(stream));
+  clha::launch_score_route(logits, bias, n_tokens, ctx->desc.n_routed, ctx->desc.top_k, route_args(*desc), topk_out,
+                           weights_out, nullptr, ctx->status_dev, 0, false, as_stream(stream));
+  return hip_check(ctx, "route");
 }
 
 CLHA_API clha_status clha_aggregate(clha_ctx* ctx, int32_t n_layers, const int32_t* layers,
@@ -985,6 +1074,9 @@ CLHA_API clha_status clha_sync(clha_ctx* ctx, void* stream) {
     if (lay >> 32)
       return fail(ctx, CLHA_ERR_NONFINITE, "layer %d: a router logit was NaN or infinite%s%s",
                   (int32_t)(uint32_t)lay, where.empty() ? "" : "; also ", where.c_str());
+    if (rec[clha::kStatusRoute])
+      return fail(ctx, CLHA_ERR_NONFINITE, "a routing: a router logit or bias was NaN or infinite%s%s",
+                  where.empty() ? "" : "; also ", where.c_str());
     return fail(ctx, CLHA_ERR_NONFINITE, "%s: a Hessian diagonal entry was NaN or infinite", where.c_str());
   }
   return fail(ctx, CLHA_ERR_NOT_PD, "%s: the damped Hessian is not positive definite", where.c_str());
@@ -1103,6 +1195,138 @@ CLHA_API clha_status clha_collect_down_hessians(clha_ctx* ctx, int32_t layer, in
   }
   it->second.fresh = false;
   return hip_check(ctx, "collect_down_hessians");
+}
+
+static clha_status check_mx(clha_ctx* ctx, const char* what, int64_t rows, int32_t cols, int32_t dtype) {
+  if (cols < 32 || cols % 32 != 0)
+    return fail(ctx, CLHA_ERR_SHAPE, "%s: %d columns are not a positive multiple of 32", what, cols);
+  if (rows < 0 || rows > clha::kMaxMxValues / cols)
+    return fail(ctx, CLHA_ERR_SHAPE, "%s: %lld rows of %d columns: at most %lld values", what, (long long)rows, cols,
+                (long long)clha::kMaxMxValues);
+  if (dtype != CLHA_F32 && dtype != CLHA_BF16) return fail(ctx, CLHA_ERR_INVALID_ARG, "%s: bad dtype", what);
+  return CLHA_OK;
+}
+
+CLHA_API clha_status clha_mx_quantize(clha_ctx* ctx, int64_t rows, int32_t cols, const void* x, int32_t x_dtype,
+                                      int64_t ld, uint8_t* codes, uint8_t* scales, void* stream) {
+  if (!ctx) return CLHA_ERR_INVALID_ARG;
+  const clha_status st = check_mx(ctx, "mx_quantize", rows, cols, x_dtype);
+  if (st != CLHA_OK) return st;
+  if (ld < cols || ld % (x_dtype == CLHA_BF16 ? 8 : 4) != 0)
+    return fail(ctx, CLHA_ERR_SHAPE, "mx_quantize: ld %lld (at least %d, whole 16-byte steps)", (long long)ld, cols);
+  if (rows == 0) return CLHA_OK;
+  if (!x || !codes || !scales) return fail(ctx, CLHA_ERR_INVALID_ARG, "mx_quantize: null pointer");
+  if (!aligned16(x) || !aligned16(codes) || !aligned4(scales))
+    return fail(ctx, CLHA_ERR_ALIGN, "mx_quantize: misaligned pointer");
+  const OnDevice on(ctx);
+  StageTimer t(ctx, CLHA_STAGE_MX_QUANTIZE, as_stream(stream));
+  clha::launch_mx_quantize(x, x_dtype == CLHA_BF16, rows, cols, ld, codes, scales, as_stream(stream));
+  return hip_check(ctx, "mx_quantize");
+}
+
+CLHA_API clha_status clha_mx_dequantize(clha_ctx* ctx, int64_t rows, int32_t cols, const uint8_t* codes,
+                                        const uint8_t* scales, void* out, int32_t out_dtype, void* stream) {
+  if (!ctx) return CLHA_ERR_INVALID_ARG;
+  const clha_status st = check_mx(ctx, "mx_dequantize", rows, cols, out_dtype);
+  if (st != CLHA_OK || rows == 0) return st;
+  if (!codes || !scales || !out) return fail(ctx, CLHA_ERR_INVALID_ARG, "mx_dequantize: null pointer");
+  if (!aligned16(out) || !aligned16(codes) || !aligned4(scales))
+    return fail(ctx, CLHA_ERR_ALIGN, "mx_dequantize: misaligned pointer");
+  const OnDevice on(ctx);
+  StageTimer t(ctx, CLHA_STAGE_MX_QUANTIZE, as_stream(stream));
+  clha::launch_mx_dequantize(codes, scales, rows, cols, out, out_dtype == CLHA_BF16, as_stream(stream));
+  return hip_check(ctx, "mx_dequantize");
+}
+
+CLHA_API clha_status clha_mx_matmul(clha_ctx* ctx, int64_t m, int32_t n, int32_t k, const uint8_t* a,
+                                    const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales, void* out,
+                                    int32_t out_dtype, void* stream) {
+  if (!ctx) return CLHA_ERR_INVALID_ARG;
+  if (k < 32 || k > clha::kMaxMxK || k % 32 != 0)
+    return fail(ctx, CLHA_ERR_SHAPE, "mx_matmul: k %d is not a multiple of 32 in 32..%d", k, clha::kMaxMxK);
+  if (n < 1 || n > clha::kMaxMxN) return fail(ctx, CLHA_ERR_SHAPE, "mx_matmul: n %d outside 1..%d", n, clha::kMaxMxN);
+  if (m < 0 || m > INT32_MAX || m > ((int64_t)1 << 40) / n)
+    return fail(ctx, CLHA_ERR_SHAPE, "mx_matmul: m %lld is out of range", (long long)m);
+  if (out_dtype != CLHA_F32 && out_dtype != CLHA_BF16) return fail(ctx, CLHA_ERR_INVALID_ARG, "mx_matmul: bad dtype");
+  if (m == 0) return CLHA_OK;
+  if (!a || !a_scales || !w || !w_scales || !out) return fail(ctx, CLHA_ERR_INVALID_ARG, "mx_matmul: null pointer");
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out) || !aligned4(a_scales) || !aligned4(w_scales))
+    return fail(ctx, CLHA_ERR_ALIGN, "mx_matmul: misaligned pointer");
+  const OnDevice on(ctx);
+  StageTimer t(ctx, CLHA_STAGE_MX_MATMUL, as_stream(stream));
+  clha::launch_mx_matmul(a, a_scales, w, w_scales, m, n, k, out, out_dtype == CLHA_BF16, as_stream(stream));
+  return hip_check(ctx, "mx_matmul");
+}
+
+// Sizes and workspace of one pass through MXFP4 experts; n >= 1, sizes checked.
+static size_t experts_layout(const clha_ctx* ctx, int64_t n, int f, void* ws, ExpertsPlan& p) {
+  const clha_moe_desc& d = ctx->desc;
+  p.n = (int32_t)n;
+  p.d = d.d;
+  p.f = f;
+  p.E = d.n_routed;
+  p.K = d.top_k;
+  p.shared = d.n_shared;
+  p.pairs = (int32_t)(n * d.top_k);
+  const int64_t all = n * (d.top_k + d.n_shared);
+  p.tile_rows = clha::experts_tile_rows(n, p.K, p.E, p.shared);
+  // full tiles, and at most one partial tile per slot that has a pair
+  p.max_tiles = (int)(all / p.tile_rows + std::min<int64_t>(p.E, p.pairs) + p.shared);
+  Carver c(ws);
+  p.xq = c.take<uint8_t>((size_t)n * d.d / 2);
+  p.xs = c.take<uint8_t>((size_t)n * d.d / 32);
+  p.blockcounts = c.take<int32_t>((size_t)clha::experts_plan_blocks(p.pairs) * p.E);
+  p.offsets = c.take<int32_t>((size_t)p.E);
+  p.order = c.take<int32_t>((size_t)p.pairs);
+  p.tiles = c.take<int32_t>((size_t)3 * p.max_tiles);
+  p.n_tiles = c.take<int32_t>(1);
+  p.hq = c.take<uint8_t>((size_t)all * f / 2);
+  p.hs = c.take<uint8_t>((size_t)all * f / 32);
+  p.ypair = c.take<float>((size_t)all * d.d);
+  return c.off;
+}
+
+static bool experts_sizes(const clha_ctx* ctx, int64_t n, int32_t f) {
+  const clha_moe_desc& d = ctx->desc;
+  return n >= 0 && n <= d.max_tokens && d.n_shared <= clha::kMaxShared &&
+         n <= clha::kMaxExpertPairs / (d.top_k + d.n_shared) && f >= 128 && f <= 8192 && f % 128 == 0;
+}
+
+CLHA_API size_t clha_mx_experts_workspace_bytes(const clha_ctx* ctx, int64_t n_tokens, int32_t f) {
+  if (!ctx || !experts_sizes(ctx, n_tokens, f) || n_tokens == 0) return 0;
+  ExpertsPlan p;
+  return experts_layout(ctx, n_tokens, f, nullptr, p);
+}
+
+CLHA_API clha_status clha_mx_experts(clha_ctx* ctx, int64_t n_tokens, int32_t f, const uint16_t* x,
+                                     const int32_t* topk, const float* weights, const uint8_t* wgu,
+                                     const uint8_t* wgu_scales, const uint8_t* wd, const uint8_t* wd_scales, void* out,
+                                     int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!ctx) return CLHA_ERR_INVALID_ARG;
+  if (!experts_sizes(ctx, n_tokens, f))
+    return fail(ctx, CLHA_ERR_SHAPE, "mx_experts: n_tokens %lld, f %d or the block's %d shared experts out of range",
+                (long long)n_tokens, f, ctx->desc.n_shared);
+  if (out_dtype != CLHA_F32 && out_dtype != CLHA_BF16) return fail(ctx, CLHA_ERR_INVALID_ARG, "mx_experts: bad dtype");
+  if (n_tokens == 0) return CLHA_OK;
+  if (!x || !topk || !weights || !wgu || !wgu_scales || !wd || !wd_scales || !out || !workspace)
+    return fail(ctx, CLHA_ERR_INVALID_ARG, "mx_experts: null pointer");
+  if (!aligned16(x) || !aligned16(wgu) || !aligned16(wd) || !aligned16(out) || !aligned16(workspace) ||
+      !aligned4(topk) || !aligned4(weights) || !aligned4(wgu_scales) || !aligned4(wd_scales))
+    return fail(ctx, CLHA_ERR_ALIGN, "mx_experts: misaligned pointer");
+  ExpertsPlan p;
+  const size_t need = experts_layout(ctx, n_tokens, f, workspace, p);
+  if (workspace_bytes < need)
+    return fail(ctx, CLHA_ERR_WORKSPACE, "mx_experts: workspace %zu < %zu bytes", workspace_bytes, need);
+  p.topk = topk;
+  p.weights = weights;
+  p.wgu = wgu;
+  p.wgu_scales = wgu_scales;
+  p.wd = wd;
+  p.wd_scales = wd_scales;
+  const OnDevice on(ctx);
+  StageTimer t(ctx, CLHA_STAGE_MX_EXPERTS, as_stream(stream));
+  clha::launch_experts(p, x, out, out_dtype == CLHA_BF16, as_stream(stream));
+  return hip_check(ctx, "mx_experts");
 }
 
 }  // extern "C"

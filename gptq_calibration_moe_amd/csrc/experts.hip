@@ -1,0 +1,259 @@
+// The pass of tokens through MXFP4 experts.
+//
+//   xq = MX(x);  for every pair (token t, slot e):  g, u = xq Wg_e^T, xq Wu_e^T
+//   h = silu(g) u in fp32;  hq = MX(h);  y_pair = hq Wd_e^T
+//   y_t = sum over the token's K routed pairs (weight w_tk, in order) + its shared pairs
+//
+// A slot is a routed expert (0 .. E-1) or a shared one (E ..), which takes every
+// token with weight 1.  Pair p = t K + k is routed, pair N K + s N + t shared.
+// Pairs are sorted by slot (position list `order`; the shared slots' positions
+// N K + s N + t are the pairs themselves), cut into tiles of one slot, and the
+// two products run tile by tile: the first writes hq by position, the second
+// y_pair by pair, so a last kernel adds a token's pairs in a fixed order and no
+// result depends on timing.  A routed id outside 0 .. E-1 stands for no expert:
+// it is in no list and adds nothing.
+#include "kernels.h"
+#include "mx_stream.h"
+
+namespace clha {
+
+// ------------------------------------------------------------------ plan
+// Counting sort of the routed pairs by slot, kPlanPairs pairs per workgroup.
+constexpr int kPlanPairs = 4096;
+
+__global__ __launch_bounds__(256) void experts_count_kernel(const int32_t* __restrict__ topk, int64_t pairs, int E,
+                                                            int32_t* __restrict__ blockcounts) {
+  __shared__ int32_t cnt[kMaxExperts];
+  for (int e = threadIdx.x; e < E; e += 256) cnt[e] = 0;
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * kPlanPairs;
+  for (int i = threadIdx.x; i < kPlanPairs; i += 256) {
+    if (base + i >= pairs) break;
+    const int e = topk[base + i];
+    if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += 256) blockcounts[(int64_t)blockIdx.x * E + e] = cnt[e];
+}
+
+// One workgroup: each block's base within its slot, the slots' offsets, and the
+// tiles: (slot, first position, rows) with at most `rows` positions each.
+__global__ __launch_bounds__(1024) void experts_scan_kernel(int32_t* __restrict__ blockcounts, int nblk, int64_t n,
+                                                            int64_t pairs, int E, int slots, int rows,
+                                                            int32_t* __restrict__ offsets, int32_t* __restrict__ tiles,
+                                                            int32_t* __restrict__ n_tiles) {
+  __shared__ int32_t total[kMaxExpertSlots + 1], first[kMaxExpertSlots + 1], tile0[kMaxExpertSlots + 1];
+  for (int e = threadIdx.x; e < slots; e += 1024) {
+    if (e < E) {
+      int32_t run = 0;
+      for (int b = 0; b < nblk; ++b) {
+        const int32_t c = blockcounts[(int64_t)b * E + e];
+        blockcounts[(int64_t)b * E + e] = run;
+        run += c;
+      }
+      total[e] = run;
+    } else {
+      total[e] = (int32_t)n;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int32_t o = 0, t = 0;
+    for (int e = 0; e < slots; ++e) {
+      first[e] = e < E ? o : (int32_t)(pairs + (int64_t)(e - E) * n);
+      if (e < E) o += total[e];
+      tile0[e] = t;
+      t += (total[e] + rows - 1) / rows;
+    }
+    *n_tiles = t;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < slots; e += 1024) {
+    if (e < E) offsets[e] = first[e];
+    for (int i = 0; i * rows < total[e]; ++i) {
+      int32_t* d = tiles + 3 * (int64_t)(tile0[e] + i);
+      d[0] = e;
+      d[1] = first[e] + i * rows;
+      d[2] = min(rows, total[e] - i * rows);
+    }
+  }
+}
+
+// order[offset + rank] = pair.  Ranks inside a block come from LDS counters in
+// whatever order: a pair's results do not depend on its place in a tile.
+__global__ __launch_bounds__(256) void experts_scatter_kernel(const int32_t* __restrict__ topk, int64_t pairs, int E,
+                                                              const int32_t* __restrict__ blockbase,
+                                                              const int32_t* __restrict__ offsets,
+                                                              int32_t* __restrict__ order) {
+  __shared__ int32_t next[kMaxExperts];
+  for (int e = threadIdx.x; e < E; e += 256) next[e] = offsets[e] + blockbase[(int64_t)blockIdx.x * E + e];
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * kPlanPairs;
+  for (int i = threadIdx.x; i < kPlanPairs; i += 256) {
+    if (base + i >= pairs) break;
+    const int e = topk[base + i];
+    if (e >= 0 && e < E) order[atomicAdd(&next[e], 1)] = (int32_t)(base + i);
+  }
+}
+
+// ------------------------------------------------------------------ products
+
+// Pair at a position, and a pair's token.
+__device__ __forceinline__ int32_t pair_at(const ExpertsPlan& p, int32_t pos) {
+  return pos < p.pairs ? p.order[pos] : pos;
+}
+__device__ __forceinline__ int32_t token_of(const ExpertsPlan& p, int32_t pair) {
+  return pair < p.pairs ? pair / p.K : (int32_t)((pair - p.pairs) % p.n);
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// First product, SwiGLU and quantization: a workgroup owns 32 features (their
+// gate and up rows: four fragments of 16) of one tile of up to 16 MF positions.
+template <int MF, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void experts_up_stream_kernel(ExpertsPlan p) {
+  __shared__ f32x4 part[WAVES][4 * MF][64];
+  if ((int)blockIdx.x >= *p.n_tiles) return;
+  const int32_t* td = p.tiles + 3 * (int64_t)blockIdx.x;
+  const int e = td[0], pos0 = td[1], rows = td[2];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
+  const int f0 = blockIdx.y * 32;
+  const int nb = p.d / kMxBlock;
+  MxRow wrow[4], xrow[MF];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {   // gate features 0-15, 16-31, then up
+    const int64_t row = (int64_t)e * 2 * p.f + (a >> 1) * p.f + f0 + 16 * (a & 1) + r;
+    wrow[a] = {p.wgu + row * nb * kMxBlockBytes, p.wgu_scales + row * nb};
+  }
+#pragma unroll
+  for (int m = 0; m < MF; ++m) {
+    const int64_t t = token_of(p, pair_at(p, pos0 + min(16 * m + r, rows - 1)));
+    xrow[m] = {p.xq + t * nb * kMxBlockBytes, p.xs + t * nb};
+  }
+  f32x4 acc[4][MF];
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int m = 0; m < MF; ++m) acc[a][m] = f32x4{0, 0, 0, 0};
+  mx_stream<4, MF>(wrow, xrow, nb, wave, WAVES, acc);
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int m = 0; m < MF; ++m) part[wave][a * MF + m][lane] = acc[a][m];
+  __syncthreads();
+  // position r of fragment m: its 32 features are in the four lanes r + 16 q,
+  // eight each (4 q + 0..3 of both halves)
+  for (int m = wave; m < MF; m += WAVES) {
+    float v[8];
+    f32x4 s[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      s[a] = part[0][a * MF + m][lane];
+#pragma unroll
+      for (int u = 1; u < WAVES; ++u) s[a] += part[u][a * MF + m][lane];
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = swiglu(s[i >> 2][i & 3], s[2 + (i >> 2)][i & 3]);
+      const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
+      top = u > top ? u : top;
+    }
+#pragma unroll
+    for (int o = 16; o < 64; o <<= 1) {
+      const uint32_t u = __shfl_xor(top, o);
+      top = u > top ? u : top;
+    }
+    const int sb = mx_scale_byte(top);
+    const uint32_t q = sb == kMxNan ? 0u : mx_codes8(v, sb);   // low half: features 4q.., high half: 16 + 4q..
+    if (16 * m + r < rows) {
+      const int64_t at = (int64_t)(pos0 + 16 * m + r) * (p.f / kMxBlock) + blockIdx.y;
+      uint16_t* dst = reinterpret_cast<uint16_t*>(p.hq + at * kMxBlockBytes);
+      dst[lane >> 4] = (uint16_t)q;
+      dst[4 + (lane >> 4)] = (uint16_t)(q >> 16);
+      if (lane < 16) p.hs[at] = (uint8_t)sb;
+    }
+  }
+}
+
+// Second product: 16 model features of one tile.
+template <int MF, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void experts_down_stream_kernel(ExpertsPlan p) {
+  __shared__ f32x4 part[WAVES][MF][64];
+  if ((int)blockIdx.x >= *p.n_tiles) return;
+  const int32_t* td = p.tiles + 3 * (int64_t)blockIdx.x;
+  const int e = td[0], pos0 = td[1], rows = td[2];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
+  const int c0 = blockIdx.y * 16;
+  const int nb = p.f / kMxBlock;
+  const int64_t wr = (int64_t)e * p.d + c0 + r;
+  const MxRow wrow[1] = {{p.wd + wr * nb * kMxBlockBytes, p.wd_scales + wr * nb}};
+  MxRow hrow[MF];
+#pragma unroll
+  for (int m = 0; m < MF; ++m) {
+    const int64_t pos = pos0 + min(16 * m + r, rows - 1);
+    hrow[m] = {p.hq + pos * nb * kMxBlockBytes, p.hs + pos * nb};
+  }
+  f32x4 acc[1][MF];
+#pragma unroll
+  for (int m = 0; m < MF; ++m) acc[0][m] = f32x4{0, 0, 0, 0};
+  mx_stream<1, MF>(wrow, hrow, nb, wave, WAVES, acc);
+#pragma unroll
+  for (int m = 0; m < MF; ++m) part[wave][m][lane] = acc[0][m];
+  __syncthreads();
+  for (int m = wave; m < MF; m += WAVES) {
+    f32x4 v = part[0][m][lane];
+#pragma unroll
+    for (int u = 1; u < WAVES; ++u) v += part[u][m][lane];
+    if (16 * m + r < rows) {
+      const int64_t pair = pair_at(p, pos0 + 16 * m + r);
+      *reinterpret_cast<f32x4*>(p.ypair + pair * p.d + c0 + 4 * (lane >> 4)) = v;
+    }
+  }
+}
+
+// y_t = sum of its pairs: the routed ones in order with their weights, then the
+// shared ones; four features per thread.
+__global__ __launch_bounds__(256) void experts_combine_kernel(ExpertsPlan p, void* __restrict__ out, bool bf16) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int quads = p.d / 4;
+  if (i >= p.n * quads) return;
+  const int64_t t = i / quads;
+  const int c = (int)(i - t * quads) * 4;
+  f32x4 y = {0, 0, 0, 0};
+  for (int k = 0; k < p.K; ++k) {
+    const int64_t pair = t * p.K + k;
+    const int e = p.topk[pair];
+    if (e < 0 || e >= p.E) continue;
+    y += p.weights[pair] * *reinterpret_cast<const f32x4*>(p.ypair + pair * p.d + c);
+  }
+  for (int s = 0; s < p.shared; ++s)
+    y += *reinterpret_cast<const f32x4*>(p.ypair + (p.pairs + (int64_t)s * p.n + t) * p.d + c);
+  if (bf16) {
+    uint2 q;
+    q.x = mx_bf16(y[0]) | ((uint32_t)mx_bf16(y[1]) << 16);
+    q.y = mx_bf16(y[2]) | ((uint32_t)mx_bf16(y[3]) << 16);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + t * p.d + c) = q;
+  } else {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + t * p.d + c) = y;
+  }
+}
+
+int experts_tile_rows(int64_t, int, int, int) { return 16; }
+int experts_plan_blocks(int64_t pairs) { return (int)((pairs + kPlanPairs - 1) / kPlanPairs); }
+
+void launch_experts(const ExpertsPlan& p, const uint16_t* x, void* out, bool bf16, hipStream_t s) {
+  launch_mx_quantize(x, true, p.n, p.d, p.d, p.xq, p.xs, s);
+  const int nblk = experts_plan_blocks(p.pairs);
+  hipLaunchKernelGGL(experts_count_kernel, dim3(nblk), dim3(256), 0, s, p.topk, p.pairs, p.E, p.blockcounts);
+  hipLaunchKernelGGL(experts_scan_kernel, dim3(1), dim3(1024), 0, s, p.blockcounts, nblk, p.n, p.pairs, p.E,
+                     p.E + p.shared, p.tile_rows, p.offsets, p.tiles, p.n_tiles);
+  hipLaunchKernelGGL(experts_scatter_kernel, dim3(nblk), dim3(256), 0, s, p.topk, p.pairs, p.E, p.blockcounts,
+                     p.offsets, p.order);
+  hipLaunchKernelGGL((experts_up_stream_kernel<1, 4>), dim3(p.max_tiles, p.f / 32), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((experts_down_stream_kernel<1, 4>), dim3(p.max_tiles, p.d / 16), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(experts_combine_kernel, dim3((unsigned)((p.n * (p.d / 4) + 255) / 256)), dim3(256), 0, s, p, out,
+                     bf16);
+}
+
+}  // namespace clha

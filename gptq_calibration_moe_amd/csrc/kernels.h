@@ -38,12 +38,15 @@ constexpr int kGemmTile = 128;        // rows and columns of a trailing-update t
 //   word 2       the same for the lowest failing Hessian of the call
 //   words 4, 5   0, or (1 << 32 | layer) of the first collection with a
 //                non-finite router logit (the first writer wins)
+//   word 6       1 when a routing without a layer (clha_route) met a non-finite
+//                logit or bias
 constexpr int kStatusNonfinite = 1;
 constexpr int kStatusNotPd = 2;
 constexpr int kStatusWords = 16;
 constexpr int kStatusJob = 1;
 constexpr int kStatusMat = 2;
 constexpr int kStatusLayer = 4;
+constexpr int kStatusRoute = 6;
 constexpr int kMaxContexts = 1024;    // live contexts per device (status records)
 // A free status record of `device` (the current device), cleared, and its slot;
 // nullptr when all kMaxContexts records are taken or the lookup fails.
@@ -195,5 +198,56 @@ double* loss_scratch(int device);        // its address on `device`, or null bef
 // ---------------------------------------------------------------- packed codes
 void launch_pack_codes(const uint8_t* codes, uint8_t* packed, int64_t n_codes, int bits, hipStream_t s);
 void launch_unpack_codes(const uint8_t* packed, uint8_t* codes, int64_t n_codes, int bits, hipStream_t s);
+
+// ---------------------------------------------------------------- routing by scores
+constexpr int kScoreSoftmax = 0, kScoreSigmoid = 1;   // clha_score
+constexpr int kGroupMax = 0, kGroupTop2 = 1;          // clha_group_score
+constexpr int64_t kMaxRouteTokens = (int64_t)1 << 27; // 16 lanes a token within one launch's threads
+struct RouteArgs {
+  int score, n_groups, top_groups, group_score, renormalize;
+  float scale;
+};
+// topk [n][K], weights [n][K] (may be null); iota (may be null) receives 0 .. n-1.  Non-finite
+// logits or biases are latched for `layer`, or as a plain routing's when has_layer is false.
+void launch_score_route(const float* logits, const float* bias, int64_t n, int E, int K, const RouteArgs& a,
+                        int32_t* topk, float* weights, int32_t* iota, int* status, int layer, bool has_layer,
+                        hipStream_t s);
+
+// ---------------------------------------------------------------- MXFP4
+constexpr int64_t kMaxMxValues = (int64_t)1 << 34;   // values of one quantize / dequantize call
+constexpr int kMaxMxK = 65536;                       // contraction length of a product
+constexpr int kMaxMxN = 524288;                      // rows of its right operand
+void launch_mx_quantize(const void* x, bool bf16, int64_t rows, int cols, int64_t ld, uint8_t* codes, uint8_t* scales,
+                        hipStream_t s);
+void launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, void* out, bool bf16,
+                          hipStream_t s);
+void launch_mx_matmul(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t m, int n, int k,
+                      void* out, bool bf16, hipStream_t s);
+
+// The pass through MXFP4 experts (layouts in experts.hip).
+constexpr int kMaxShared = 256;                            // shared experts of one pass
+constexpr int kMaxExpertSlots = kMaxExperts + kMaxShared;  // routed and shared experts
+constexpr int64_t kMaxExpertPairs = (int64_t)1 << 27;      // (token, expert) pairs of one pass
+struct ExpertsPlan {
+  int32_t n, d, f, E, K, shared;
+  int32_t pairs;                 // n * K routed pairs
+  int tile_rows;                 // positions of a tile
+  int max_tiles;
+  const int32_t* topk;           // [n][K]
+  const float* weights;          // [n][K]
+  const uint8_t *wgu, *wgu_scales, *wd, *wd_scales;
+  // workspace
+  uint8_t *xq, *xs;              // x in MXFP4: [n][d/2], [n][d/32]
+  int32_t* blockcounts;          // [plan blocks][E]
+  int32_t* offsets;              // [E] first position of a routed slot
+  int32_t* order;                // [pairs] pair at each position of the routed slots
+  int32_t* tiles;                // [max_tiles][3] slot, first position, positions
+  int32_t* n_tiles;
+  uint8_t *hq, *hs;              // h in MXFP4 by position: [all pairs][f/2], [all pairs][f/32]
+  float* ypair;                  // [all pairs][d] by pair
+};
+int experts_plan_blocks(int64_t pairs);
+int experts_tile_rows(int64_t n, int K, int E, int shared);
+void launch_experts(const ExpertsPlan& p, const uint16_t* x, void* out, bool bf16, hipStream_t s);
 
 }  // namespace clha

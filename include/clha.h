@@ -148,6 +148,54 @@ CLHA_API clha_status clha_collect_hessians(clha_ctx* ctx, int32_t layer, int64_t
                                            int32_t* token_ids_out,
                                            void* workspace, size_t workspace_bytes, void* stream);
 
+/* Scores a routing is made by. */
+typedef enum clha_score { CLHA_SCORE_SOFTMAX = 0, CLHA_SCORE_SIGMOID = 1 } clha_score;
+
+/* What ranks the groups of a grouped routing: a group's largest choice, or the sum of its two
+ * largest (of a group of one expert: that one). */
+typedef enum clha_group_score { CLHA_GROUP_MAX = 0, CLHA_GROUP_TOP2 = 1 } clha_group_score;
+
+/* How tokens choose experts by scores (the block's E experts, K per token):
+ *   s_e = softmax over all E logits, or sigmoid(l_e);
+ *   c_e = s_e + bias_e with a bias; without one the choices are ordered as the logits are;
+ *   n_groups > 1: experts g*E/n_groups .. (g+1)*E/n_groups - 1 are group g, marked by group_score
+ *     of c (without a bias: the largest logit, or the sum of the two largest scores); the
+ *     top_groups groups with the largest marks stay, ties to the lower group;
+ *   the K largest c of the experts that stay, larger first, ties to the lower index;
+ *   w_k = s of the k-th chosen expert (without the bias), divided by the sum of the K chosen s
+ *     when renormalize is set (0 where that sum is 0), times scale.
+ * c and the marks are compared in 64 bits, weights are formed in 64 bits and rounded once. */
+typedef struct clha_route_desc {
+  int32_t score;        /* clha_score */
+  int32_t n_groups;     /* 1 (no groups) or a divisor of E */
+  int32_t top_groups;   /* 1..n_groups; top_groups * E/n_groups >= K */
+  int32_t group_score;  /* clha_group_score; read when n_groups > 1 */
+  int32_t renormalize;  /* 0 or 1 */
+  float scale;          /* finite */
+} clha_route_desc;
+
+/* Routes n_tokens tokens by scores, for a block whose experts are chosen that way (the choice of
+ * clha_collect_hessians is the K largest logits, with no weights).
+ *   logits       device, float [n_tokens][E]
+ *   bias         device, float [E], or NULL
+ *   topk_out     device, int32 [n_tokens][K]
+ *   weights_out  device, float [n_tokens][K], or NULL
+ * Non-finite logits or biases latch CLHA_ERR_NONFINITE; such a token's experts are then
+ * undefined, but distinct and in 0..E-1.
+ * Errors: INVALID_ARG (null pointer, unknown enum, scale not finite), SHAPE (groups, n_tokens
+ * outside 0..2^27), ALIGN (4 bytes).  n_tokens == 0 enqueues nothing and reads no pointer. */
+CLHA_API clha_status clha_route(clha_ctx* ctx, const clha_route_desc* desc, int64_t n_tokens, const float* logits,
+                                const float* bias, int32_t* topk_out, float* weights_out, void* stream);
+
+/* clha_collect_hessians for a block that routes by scores: step 1 is clha_route's choice (with its
+ * optional weights); everything else is as documented there, the workspace included.  A non-finite
+ * bias is latched like a logit. */
+CLHA_API clha_status clha_collect_hessians_scored(clha_ctx* ctx, int32_t layer, const clha_route_desc* desc,
+                                                  int64_t n_tokens, const uint16_t* x, const float* logits,
+                                                  const float* bias, int32_t* topk_out, float* weights_out,
+                                                  int64_t* offsets_out, int32_t* token_ids_out, void* workspace,
+                                                  size_t workspace_bytes, void* stream);
+
 /* Aggregation phase (section 2.1 Proposition 1, section 2.2 phase 2) over the given
  * layers, for every slot e:
  *   ROUTING_FREQ: H[e] = (sum_i S_i[e]) / (sum_i n_i[e])
@@ -356,6 +404,69 @@ CLHA_API clha_status clha_pack_codes(clha_ctx* ctx, int64_t n_codes, int32_t bit
 CLHA_API clha_status clha_unpack_codes(clha_ctx* ctx, int64_t n_codes, int32_t bits, const uint8_t* packed,
                                        uint8_t* codes, void* stream);
 
+/* MXFP4, the OCP microscaled 4-bit format that the matrix cores multiply directly: an
+ * alternative to GPTQ's integer grids for storing experts and for running them.  Blocks of 32
+ * values of a row share a scale 2^e, stored as the byte e + 127 (255: the block is NaN); a value
+ * is a 4-bit e2m1 code (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign in bit 3), two to a byte, the even
+ * element in the low half.  A matrix [rows][cols], cols a multiple of 32, is
+ *   codes   uint8 [rows][cols/2], 16-byte aligned
+ *   scales  uint8 [rows][cols/32]; 4-byte aligned
+ * These calls use only the context's device, status and timers, not its block shape (except
+ * clha_mx_experts). */
+
+/* Quantizes: e = floor(log2(largest magnitude of the block)) - 2, at least -127; codes are the
+ * nearest of x 2^-e, ties to the even code, saturated at 6.  A block that holds a NaN or an
+ * infinity becomes the NaN block (scale 255, codes 0); a block of zeros has scale byte 0.
+ *   x      device, [rows][ld] fp32 or bf16 (x_dtype), columns 0..cols-1 of each row
+ *   ld     elements between rows, >= cols, a multiple of 4 (fp32) or 8 (bf16)
+ *   rows * cols at most 2^34; rows == 0 enqueues nothing and reads no pointer
+ * Errors: INVALID_ARG, SHAPE, ALIGN, HIP. */
+CLHA_API clha_status clha_mx_quantize(clha_ctx* ctx, int64_t rows, int32_t cols, const void* x, int32_t x_dtype,
+                                      int64_t ld, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The values that codes and scales stand for, [rows][cols] fp32 or bf16 (out_dtype, 16-byte
+ * aligned); exact in both types but for overflow past the type's range.  Sizes and errors as
+ * clha_mx_quantize. */
+CLHA_API clha_status clha_mx_dequantize(clha_ctx* ctx, int64_t rows, int32_t cols, const uint8_t* codes,
+                                        const uint8_t* scales, void* out, int32_t out_dtype, void* stream);
+
+/* Product y[i][j] = sum_l a[i][l] w[j][l] of two MXFP4 matrices: fp32 sums in an order that
+ * depends on the sizes only, one rounding to the output type.
+ *   a   [m][k], w [n][k] in MXFP4; m >= 0, n 1..524288, k a multiple of 32, 32..65536
+ *   out device, [m][n] fp32 or bf16 (out_dtype), 16-byte aligned
+ * A NaN block makes the row (of a) or column (of w) NaN.  m == 0 enqueues nothing and reads no
+ * pointer.  m * n at most 2^40, m at most 2^31 - 1.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, HIP. */
+CLHA_API clha_status clha_mx_matmul(clha_ctx* ctx, int64_t m, int32_t n, int32_t k, const uint8_t* a,
+                                    const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales, void* out,
+                                    int32_t out_dtype, void* stream);
+
+/* Device workspace bytes clha_mx_experts needs for n_tokens tokens and intermediate size f. */
+CLHA_API size_t clha_mx_experts_workspace_bytes(const clha_ctx* ctx, int64_t n_tokens, int32_t f);
+
+/* The pass of tokens through the block's experts, held in MXFP4 (E routed experts, then the
+ * n_shared shared ones):
+ *   xq = MX(x);  per token t and expert e of it:  g = xq Wg_e^T,  u = xq Wu_e^T (fp32 sums)
+ *   h = silu(g) u (fp32, as clha_collect_down_hessians defines it, not rounded to bf16);  hq = MX(h)
+ *   y_t = sum_k weights[t][k] (hq Wd_e^T), e = topk[t][k], in the order of k, then the shared
+ *         experts' with weight 1 (fp32); one rounding to the output type.
+ * MX(.) is clha_mx_quantize.
+ *   x        device, bf16 bits [n_tokens][d]; n_tokens 0..max_tokens, at most 2^27 / (K + n_shared)
+ *   topk     device, int32 [n_tokens][K]; an id outside 0..E-1 stands for no expert and adds
+ *            nothing; the same expert twice counts twice
+ *   weights  device, float [n_tokens][K]
+ *   wgu      [E + n_shared][2f][d] in MXFP4: gate rows 0..f-1, up rows f..2f-1
+ *   wd       [E + n_shared][d][f] in MXFP4
+ *   f        multiple of 128, 128..8192; n_shared at most 256
+ *   out      device, [n_tokens][d] fp32 or bf16 (out_dtype), 16-byte aligned
+ * Results do not depend on timing.  Calls that share a workspace must be ordered on one stream.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, WORKSPACE, HIP.  n_tokens == 0 enqueues nothing and reads
+ * no pointer. */
+CLHA_API clha_status clha_mx_experts(clha_ctx* ctx, int64_t n_tokens, int32_t f, const uint16_t* x,
+                                     const int32_t* topk, const float* weights, const uint8_t* wgu,
+                                     const uint8_t* wgu_scales, const uint8_t* wd, const uint8_t* wd_scales, void* out,
+                                     int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Stages timed by the optional per-stage timers. */
 typedef enum clha_stage {
   CLHA_STAGE_ROUTE = 0,      /* top-K routing kernel */
@@ -367,7 +478,10 @@ typedef enum clha_stage {
   CLHA_STAGE_GPTQ = 6,       /* clha_gptq_quantize: factorisation and GPTQ, which overlap */
   CLHA_STAGE_LOSS = 7,       /* explicit loss kernels */
   CLHA_STAGE_SYRK_REDUCE = 8, /* Gram sums: partial sums of token-split slots into S, empty slots zeroed */
-  CLHA_NUM_STAGES = 9
+  CLHA_STAGE_MX_QUANTIZE = 9, /* clha_mx_quantize, clha_mx_dequantize */
+  CLHA_STAGE_MX_MATMUL = 10, /* clha_mx_matmul */
+  CLHA_STAGE_MX_EXPERTS = 11, /* clha_mx_experts, all of its kernels */
+  CLHA_NUM_STAGES = 12
 } clha_stage;
 
 /* Enables (1) or disables (0) per-stage timing: each stage of each later call records a

@@ -487,3 +487,122 @@ def calibrate_pair(x_bits_list, logits_list, jobs: dict, *, n_routed: int, top_k
                 loss(w, g["wq"], S[s] / n[s]) if n[s] > 0 else 0.0
                 for S, n in zip(out["S"], out["n"])]
     return out
+
+
+# --------------------------------------------------------------------------- routing by scores
+
+def route_scores(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+                 group_score: str = "max", renormalize: bool = True, scale: float = 1.0):
+    """Experts by scores in fp64: (topk [n, k], weights [n, k]).  s = softmax or sigmoid of the
+    logits; the choice is s + bias, or in the logits' order without a bias; with groups only the
+    top_groups groups of the largest mark stay; larger choice first, ties to the lower index."""
+    l = np.asarray(logits, np.float64)
+    n, e = l.shape
+    if score == "softmax":
+        s = np.exp(l - l.max(axis=1, keepdims=True))
+        s /= s.sum(axis=1, keepdims=True)
+    else:
+        with np.errstate(over="ignore"):
+            s = 1.0 / (1.0 + np.exp(-l))
+    choice = l if bias is None else s + np.asarray(bias, np.float64)
+    if groups > 1:
+        per = e // groups
+        by = (s if bias is None and group_score == "top2" else choice).reshape(n, groups, per)
+        ranked = -np.sort(-by, axis=2)
+        mark = ranked[:, :, 0] if group_score == "max" else ranked[:, :, :2].sum(axis=2)
+        best = np.argsort(-mark, axis=1, kind="stable")[:, :top_groups]
+        keep = np.zeros((n, groups), bool)
+        np.put_along_axis(keep, best, True, axis=1)
+        choice = np.where(np.repeat(keep, per, axis=1), choice, -np.inf)
+    topk = np.argsort(-choice, axis=1, kind="stable")[:, :k]
+    w = np.take_along_axis(s, topk, axis=1)
+    if renormalize:
+        if score == "softmax":      # relative to the largest chosen logit: the same ratio, never 0/0
+            lc = np.take_along_axis(l, topk, axis=1)
+            w = np.exp(lc - lc.max(axis=1, keepdims=True))
+        total = w.sum(axis=1, keepdims=True)
+        w = np.where(total > 0, w / np.where(total > 0, total, 1.0), 0.0)
+    return topk.astype(np.int32), w * scale
+
+
+# --------------------------------------------------------------------------- MXFP4
+
+MX_LEVELS = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def mx_scale(amax) -> np.ndarray:
+    """Scale bytes of blocks with these largest magnitudes (fp64)."""
+    amax = np.asarray(amax, np.float64)
+    ok = np.isfinite(amax)
+    e = np.frexp(np.where(ok & (amax > 0), amax, 1.0))[1] - 3          # floor(log2 amax) - 2
+    b = np.clip(np.where(amax > 0, e, -127), -127, 127) + 127
+    return np.where(ok, b, 255).astype(np.uint8)
+
+
+def mx_round(x, scales):
+    """Codes (uint8, one per value) of x [..., cols] at given scales [..., cols/32]."""
+    x = np.asarray(x, np.float64)
+    sc = np.repeat(np.asarray(scales).astype(np.int64), 32, axis=-1)
+    with np.errstate(invalid="ignore", over="ignore"):
+        a = np.abs(np.ldexp(x, 127 - sc))
+        code = np.zeros(x.shape, np.int64)
+        for i in range(7):
+            mid = 0.5 * (MX_LEVELS[i] + MX_LEVELS[i + 1])
+            code += (a >= mid) if i % 2 else (a > mid)                # a tie goes to the even code
+    code = np.where(np.signbit(x), code + 8, code)
+    return np.where(sc == 255, 0, code).astype(np.uint8)
+
+
+def mx_quantize(x):
+    """(codes uint8 [..., cols/2], scales uint8 [..., cols/32])."""
+    x = np.asarray(x, np.float64)
+    with np.errstate(invalid="ignore"):
+        scales = mx_scale(np.abs(x).reshape(*x.shape[:-1], -1, 32).max(axis=-1))
+    c = mx_round(x, scales)
+    return c[..., 0::2] | (c[..., 1::2] << 4), scales
+
+
+def mx_values(codes, scales) -> np.ndarray:
+    """fp64 values of MXFP4 codes and scales."""
+    codes = np.asarray(codes)
+    c = np.empty((*codes.shape[:-1], 2 * codes.shape[-1]), np.int64)
+    c[..., 0::2], c[..., 1::2] = codes & 15, codes >> 4
+    s = np.repeat(np.asarray(scales).astype(np.int64), 32, axis=-1)
+    v = np.ldexp(MX_LEVELS[c & 7] * np.where(c > 7, -1.0, 1.0), s - 127)
+    return np.where(s == 255, np.nan, v)
+
+
+def mx_experts(x, topk, weights, wgu, wd, n_routed: int, sum_eps: float = 0.0):
+    """The pass through MXFP4 experts in fp64; x fp64 [n, d], wgu fp64 [slots, 2f, d] and wd
+    [slots, d, f] (values).  Returns (y, tol): tol bounds how far y may move when every product
+    is summed with relative error sum_eps of its absolute sum and h is formed in fp32, including
+    the codes of h that such an error can turn (h is rounded to 4 bits, so a value next to a
+    border may go either way)."""
+    x = mx_values(*mx_quantize(x))
+    n, f, slots = x.shape[0], wd.shape[2], wd.shape[0]
+    y, tol = np.zeros((n, wd.shape[1])), np.zeros((n, wd.shape[1]))
+    for e in range(slots):
+        w = np.ones(n)
+        t = np.arange(n)
+        if e < n_routed:
+            w = (np.asarray(weights, np.float64) * (topk == e)).sum(axis=1)
+            t = np.nonzero((topk == e).any(axis=1))[0]
+        if t.size == 0:
+            continue
+        gu = x[t] @ wgu[e].T
+        err = sum_eps * (np.abs(x[t]) @ np.abs(wgu[e]).T)
+        g, u, eg, eu = gu[:, :f], gu[:, f:], err[:, :f], err[:, f:]
+        sl = silu(g)
+        h = sl * u
+        # |silu'| <= 1.1; exp, division and two products in fp32: 8 units in the last place
+        dh = 1.1 * eg * (np.abs(u) + eu) + np.abs(sl) * eu + (8 * 2.0 ** -24) * np.abs(h)
+        lo, hi = h - dh, h + dh
+        top = lambda a: np.abs(a).reshape(t.size, -1, 32).max(axis=2)          # noqa: E731
+        q = [mx_values(c[..., 0::2] | (c[..., 1::2] << 4), s)
+             for s in (mx_scale(top(h)), mx_scale(np.maximum(top(lo), top(hi))),
+                       mx_scale(np.maximum(top(h) - top(dh), 0)))
+             for c in (mx_round(h, s), mx_round(lo, s), mx_round(hi, s))]
+        spread = np.max(q, axis=0) - np.min(q, axis=0)
+        y[t] += w[t, None] * (q[0] @ wd[e].T)
+        tol[t] += np.abs(w[t, None]) * (spread @ np.abs(wd[e]).T + sum_eps * (np.abs(q[0]) @ np.abs(wd[e]).T))
+    return y, tol
