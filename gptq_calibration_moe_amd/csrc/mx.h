@@ -15,6 +15,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace clha {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
