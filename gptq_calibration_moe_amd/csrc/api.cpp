@@ -1269,7 +1269,7 @@ static size_t experts_layout(const clha_ctx* ctx, int64_t n, int f, void* ws, Ex
   p.shared = d.n_shared;
   p.pairs = (int32_t)(n * d.top_k);
   const int64_t all = n * (d.top_k + d.n_shared);
-  p.tile_rows = clha::experts_tile_rows(n, p.K, p.E, p.shared);
+  p.tile_rows = clha::experts_tile_rows(n, p.d, p.f, p.K, p.E);
   // full tiles, and at most one partial tile per slot that has a pair
   p.max_tiles = (int)(all / p.tile_rows + std::min<int64_t>(p.E, p.pairs) + p.shared);
   Carver c(ws);
@@ -1289,7 +1289,7 @@ static size_t experts_layout(const clha_ctx* ctx, int64_t n, int f, void* ws, Ex
 static bool experts_sizes(const clha_ctx* ctx, int64_t n, int32_t f) {
   const clha_moe_desc& d = ctx->desc;
   return n >= 0 && n <= d.max_tokens && d.n_shared <= clha::kMaxShared &&
-         n <= clha::kMaxExpertPairs / (d.top_k + d.n_shared) && f >= 128 && f <= 8192 && f % 128 == 0;
+         n <= clha::kMaxExpertPairs / (d.top_k + d.n_shared) && n <= clha::kMaxExpertValues / d.d && f >= 128 && f <= 8192 && f % 128 == 0;
 }
 
 CLHA_API size_t clha_mx_experts_workspace_bytes(const clha_ctx* ctx, int64_t n_tokens, int32_t f) {

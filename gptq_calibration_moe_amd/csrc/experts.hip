@@ -14,6 +14,7 @@
 // it is in no list and adds nothing.
 #include "kernels.h"
 #include "mx_stream.h"
+#include "mx_tile.h"
 
 namespace clha {
 
@@ -212,6 +213,111 @@ __global__ __launch_bounds__(64 * WAVES) void experts_down_stream_kernel(Experts
   }
 }
 
+// ------------------------------------------------------------------ products over many positions
+// One tile of mx_tile.h per workgroup: TM positions of a tile of the plan by TN rows
+// of W.  Workgroup b runs on die b % kXcds; a die takes a contiguous run of the
+// (position tile, row tile) pairs, row tiles fastest, so what it runs together is a few
+// position tiles of one slot against all of that slot's weights, which its L2 holds.
+struct TileAt {
+  int tile, part;
+  bool any;
+};
+__device__ __forceinline__ TileAt experts_tile_at(const ExpertsPlan& p, int parts) {
+  const int64_t total = (int64_t)*p.n_tiles * parts, per = (total + kXcds - 1) / kXcds;
+  const int64_t i = blockIdx.x / kXcds, L = (int64_t)(blockIdx.x % kXcds) * per + i;
+  return {(int)(L / parts), (int)(L % parts), i < per && L < total};
+}
+
+// First product: a wave's rows of W are FN/2 fragments of gate rows and the up rows
+// of the same features, so a lane holds both values of 16 features of a block of 32 and
+// its partner (lane ^ 32) the other 16: SwiGLU and quantization stay in registers.
+template <class T, bool WORDS>
+__global__ __launch_bounds__(T::kThreads) void experts_up_tile_kernel(ExpertsPlan p) {
+  MX_TILE_LDS(T);
+  constexpr int kFeatures = T::TN / 2, kWaveFeatures = kFeatures / T::WN;
+  const TileAt at = experts_tile_at(p, p.f / kFeatures);
+  if (!at.any) return;
+  const int32_t* td = p.tiles + 3 * (int64_t)at.tile;
+  const int e = td[0], pos0 = td[1], rows = td[2];
+  const int f0 = at.part * kFeatures, nb = p.d / kMxBlock, hb = p.f / kMxBlock;
+  const MxOperand W{p.wgu + (int64_t)e * 2 * p.f * nb * kMxBlockBytes, p.wgu_scales + (int64_t)e * 2 * p.f * nb};
+  const MxOperand X{p.xq, p.xs};
+  f32x16 acc[T::FN][T::FM];
+#pragma unroll
+  for (int i = 0; i < T::FN; ++i)
+#pragma unroll
+    for (int j = 0; j < T::FM; ++j) acc[i][j] = f32x16{};
+  auto wrow = [&](int r) {
+    const int in = r % (2 * kWaveFeatures), up = in / kWaveFeatures;
+    return up * p.f + f0 + r / (2 * kWaveFeatures) * kWaveFeatures + in % kWaveFeatures;
+  };
+  auto xrow = [&](int r) { return token_of(p, pair_at(p, pos0 + min(r, rows - 1))); };
+  mx_tile_products<T, WORDS>(W, X, wrow, xrow, nb, MX_TILE_ARGS, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, g = lane >> 5;
+  const int block0 = (f0 + wave / T::WM * kWaveFeatures) / kMxBlock;
+#pragma unroll
+  for (int b = 0; b < T::FM; ++b) {
+    const int row = (wave % T::WM * T::FM + b) * 32 + r;
+    const int64_t to = (int64_t)(pos0 + row) * hb + block0;
+#pragma unroll
+    for (int a = 0; a < T::FN / 2; ++a) {
+      float h[16];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        h[i] = swiglu(acc[a][b][i], acc[T::FN / 2 + a][b][i]);
+        const uint32_t u = __float_as_uint(h[i]) & 0x7fffffffu;
+        top = u > top ? u : top;
+      }
+      const uint32_t other = __shfl_xor(top, 32);
+      const int sb = mx_scale_byte(other > top ? other : top);
+      // 16 bits for each q = i / 4: features 8 q + 4 g + 0..3 of the block
+      const uint32_t q01 = sb == kMxNan ? 0u : mx_codes8(h, sb), q23 = sb == kMxNan ? 0u : mx_codes8(h + 8, sb);
+      // lane g = 0 writes q 0 and 1 of both halves, its partner q 2 and 3
+      const uint32_t mine = g ? q23 : q01, theirs = __shfl_xor(g ? q01 : q23, 32);
+      const uint32_t lo = g ? theirs : mine, hi = g ? mine : theirs;
+      if (row < rows) {
+        *reinterpret_cast<uint2*>(p.hq + (to + a) * kMxBlockBytes + 8 * g) =
+            make_uint2((lo & 0xffffu) | (hi << 16), (lo >> 16) | (hi & 0xffff0000u));
+        if (g == 0) p.hs[to + a] = (uint8_t)sb;
+      }
+    }
+  }
+}
+
+// Second product: y_pair in fp32, rows stored by pair.
+template <class T, bool WORDS>
+__global__ __launch_bounds__(T::kThreads) void experts_down_tile_kernel(ExpertsPlan p) {
+  MX_TILE_LDS(T);
+  const int parts = (p.d + T::TN - 1) / T::TN;
+  const TileAt at = experts_tile_at(p, parts);
+  if (!at.any) return;
+  const int32_t* td = p.tiles + 3 * (int64_t)at.tile;
+  const int e = td[0], pos0 = td[1], rows = td[2];
+  const int c0 = at.part * T::TN, nb = p.f / kMxBlock;
+  const MxOperand W{p.wd + ((int64_t)e * p.d + c0) * nb * kMxBlockBytes, p.wd_scales + ((int64_t)e * p.d + c0) * nb};
+  const MxOperand X{p.hq + (int64_t)pos0 * nb * kMxBlockBytes, p.hs + (int64_t)pos0 * nb};
+  f32x16 acc[T::FN][T::FM];
+#pragma unroll
+  for (int i = 0; i < T::FN; ++i)
+#pragma unroll
+    for (int j = 0; j < T::FM; ++j) acc[i][j] = f32x16{};
+  const int last = p.d - 1 - c0;
+  auto wrow = [&](int r) { return min(r, last); };
+  auto xrow = [&](int r) { return min(r, rows - 1); };
+  mx_tile_products<T, WORDS>(W, X, wrow, xrow, nb, MX_TILE_ARGS, acc);
+  mx_meet<0>();   // the buffers become the waves' output regions
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row0 = wave % T::WM * T::FM * 32, col0 = c0 + wave / T::WM * T::FN * 32;
+  mx_tile_rows<T>(mx_region<T>(wave, MX_TILE_ARGS), acc, [&](int row, int col, f32x4 lo, f32x4 hi) {
+    if (row0 + row < rows && col0 + col < p.d) {
+      f32x4* o = reinterpret_cast<f32x4*>(p.ypair + (int64_t)pair_at(p, pos0 + row0 + row) * p.d + col0 + col);
+      o[0] = lo;
+      o[1] = hi;
+    }
+  });
+}
+
 // y_t = sum of its pairs: the routed ones in order with their weights, then the
 // shared ones; four features per thread.
 __global__ __launch_bounds__(256) void experts_combine_kernel(ExpertsPlan p, void* __restrict__ out, bool bf16) {
@@ -239,8 +345,33 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(ExpertsPlan p, voi
   }
 }
 
-int experts_tile_rows(int64_t, int, int, int) { return 16; }
+// Positions of a tile of the plan, from the mean number of a routed slot's positions
+// (the load is not known on the host): how many rows of x a slot's weights meet.  The
+// largest tile has no registers for scale rows under 16 bytes (d or f under 512).
+typedef MxTile<2, 4, 4, 2> Tile256;   // 256 rows of W by 256 positions, 8 waves
+typedef MxTile<2, 2, 2, 2> Tile128;
+int experts_tile_rows(int64_t n, int d, int f, int K, int E) {
+  const int64_t mean = n * K / E;
+  if (mean >= 192 && mx_words(d / kMxBlock) && mx_words(f / kMxBlock)) return 256;
+  return mean >= 48 ? 128 : mean >= 8 ? 64 : 16;
+}
 int experts_plan_blocks(int64_t pairs) { return (int)((pairs + kPlanPairs - 1) / kPlanPairs); }
+
+namespace {
+template <class T, bool UP, bool DOWN>   // whether the rows' scales of each product are whole words
+void run_tiles(const ExpertsPlan& p, hipStream_t s) {
+  const int64_t up = (int64_t)p.max_tiles * (p.f / (T::TN / 2)), down = (int64_t)p.max_tiles * ((p.d + T::TN - 1) / T::TN);
+  hipLaunchKernelGGL((experts_up_tile_kernel<T, UP>), dim3((unsigned)((up + kXcds - 1) / kXcds * kXcds)),
+                     dim3(T::kThreads), 0, s, p);
+  hipLaunchKernelGGL((experts_down_tile_kernel<T, DOWN>), dim3((unsigned)((down + kXcds - 1) / kXcds * kXcds)),
+                     dim3(T::kThreads), 0, s, p);
+}
+template <int MF, int WAVES>
+void run_stream(const ExpertsPlan& p, hipStream_t s) {
+  hipLaunchKernelGGL((experts_up_stream_kernel<MF, WAVES>), dim3(p.max_tiles, p.f / 32), dim3(64 * WAVES), 0, s, p);
+  hipLaunchKernelGGL((experts_down_stream_kernel<MF, WAVES>), dim3(p.max_tiles, p.d / 16), dim3(64 * WAVES), 0, s, p);
+}
+}  // namespace
 
 void launch_experts(const ExpertsPlan& p, const uint16_t* x, void* out, bool bf16, hipStream_t s) {
   launch_mx_quantize(x, true, p.n, p.d, p.d, p.xq, p.xs, s);
@@ -250,8 +381,19 @@ void launch_experts(const ExpertsPlan& p, const uint16_t* x, void* out, bool bf1
                      p.E + p.shared, p.tile_rows, p.offsets, p.tiles, p.n_tiles);
   hipLaunchKernelGGL(experts_scatter_kernel, dim3(nblk), dim3(256), 0, s, p.topk, p.pairs, p.E, p.blockcounts,
                      p.offsets, p.order);
-  hipLaunchKernelGGL((experts_up_stream_kernel<1, 4>), dim3(p.max_tiles, p.f / 32), dim3(256), 0, s, p);
-  hipLaunchKernelGGL((experts_down_stream_kernel<1, 4>), dim3(p.max_tiles, p.d / 16), dim3(256), 0, s, p);
+  switch (p.tile_rows) {
+    case 256: run_tiles<Tile256, true, true>(p, s); break;
+    case 128: {
+      const bool up = mx_words(p.d / kMxBlock), down = mx_words(p.f / kMxBlock);
+      if (up && down) run_tiles<Tile128, true, true>(p, s);
+      else if (up) run_tiles<Tile128, true, false>(p, s);
+      else if (down) run_tiles<Tile128, false, true>(p, s);
+      else run_tiles<Tile128, false, false>(p, s);
+      break;
+    }
+    case 64: run_stream<4, 4>(p, s); break;
+    default: run_stream<1, 4>(p, s); break;
+  }
   hipLaunchKernelGGL(experts_combine_kernel, dim3((unsigned)((p.n * (p.d / 4) + 255) / 256)), dim3(256), 0, s, p, out,
                      bf16);
 }

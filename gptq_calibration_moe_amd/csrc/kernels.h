@@ -228,6 +228,7 @@ void launch_mx_matmul(const uint8_t* a, const uint8_t* as, const uint8_t* w, con
 constexpr int kMaxShared = 256;                            // shared experts of one pass
 constexpr int kMaxExpertSlots = kMaxExperts + kMaxShared;  // routed and shared experts
 constexpr int64_t kMaxExpertPairs = (int64_t)1 << 27;      // (token, expert) pairs of one pass
+constexpr int64_t kMaxExpertValues = (int64_t)1 << 33;     // values of x of one pass: its codes stay within 32-bit offsets
 struct ExpertsPlan {
   int32_t n, d, f, E, K, shared;
   int32_t pairs;                 // n * K routed pairs
@@ -247,7 +248,7 @@ struct ExpertsPlan {
   float* ypair;                  // [all pairs][d] by pair
 };
 int experts_plan_blocks(int64_t pairs);
-int experts_tile_rows(int64_t n, int K, int E, int shared);
+int experts_tile_rows(int64_t n, int d, int f, int K, int E);
 void launch_experts(const ExpertsPlan& p, const uint16_t* x, void* out, bool bf16, hipStream_t s);
 
 }  // namespace clha

@@ -52,9 +52,15 @@ __device__ __forceinline__ int mx_scale_byte(uint32_t amax_bits) {
 }
 
 __device__ __forceinline__ uint16_t mx_bf16(float v) {   // round to nearest even; NaN stays NaN
-  const uint32_t b = __float_as_uint(v);
-  if ((b & 0x7fffffffu) > 0x7f800000u) return (uint16_t)((b >> 16) | 0x40u);
-  return (uint16_t)((b + 0x7fffu + ((b >> 16) & 1u)) >> 16);
+  return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// Two values in one word, the first low: the hardware's rounding conversion
+// (to nearest even, NaN stays NaN).
+__device__ __forceinline__ uint32_t mx_bf16_pair(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
 }
 
 // Codes of eight values at a block's scale byte (not NaN), half to even,

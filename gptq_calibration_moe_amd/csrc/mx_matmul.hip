@@ -52,28 +52,29 @@ __global__ __launch_bounds__(64 * WAVES) void mx_matmul_stream_kernel(const uint
   }
 }
 
-// Eight results of a row from column col: one or two 16-byte stores where the
-// row's columns allow, single elements at a ragged edge.
-__device__ __forceinline__ void mx_put8(void* out, bool bf16, int64_t row, int64_t n, int col, const float* v) {
-  const int64_t at = row * n + col;
-  if (col + 8 <= n && (n & 7) == 0) {
-    if (bf16) {
-      uint4 q;
-      q.x = mx_bf16(v[0]) | ((uint32_t)mx_bf16(v[1]) << 16);
-      q.y = mx_bf16(v[2]) | ((uint32_t)mx_bf16(v[3]) << 16);
-      q.z = mx_bf16(v[4]) | ((uint32_t)mx_bf16(v[5]) << 16);
-      q.w = mx_bf16(v[6]) | ((uint32_t)mx_bf16(v[7]) << 16);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = q;
-    } else {
-      f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(out) + at);
-      o[0] = f32x4{v[0], v[1], v[2], v[3]};
-      o[1] = f32x4{v[4], v[5], v[6], v[7]};
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (col + q < n) mx_put(out, bf16, at + q, v[q]);
+// Eight results of a row from column col: 16-byte stores where the row's columns
+// allow, single elements at a ragged edge.
+__device__ __forceinline__ void mx_put8(float* out, int64_t row, int64_t n, int col, f32x4 lo, f32x4 hi) {
+  float* o = out + row * n + col;
+  if (col + 8 <= n && (n & 3) == 0) {
+    reinterpret_cast<f32x4*>(o)[0] = lo;
+    reinterpret_cast<f32x4*>(o)[1] = hi;
+    return;
   }
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (col + q < n) o[q] = q < 4 ? lo[q] : hi[q - 4];
+}
+__device__ __forceinline__ void mx_put8(uint16_t* out, int64_t row, int64_t n, int col, uint4 v) {
+  uint16_t* o = out + row * n + col;
+  if (col + 8 <= n && (n & 7) == 0) {
+    *reinterpret_cast<uint4*>(o) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (col + q < n) o[q] = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
 }
 
 // Many rows: one tile of mx_tile.h per workgroup.  Workgroup b runs on die
@@ -88,8 +89,7 @@ __global__ __launch_bounds__(T::kThreads) void mx_matmul_tile_kernel(const uint8
                                                                      const uint8_t* __restrict__ ws, int64_t m, int n,
                                                                      int nb, int mt, int nt, void* __restrict__ out,
                                                                      bool bf16) {
-  __shared__ __attribute__((aligned(1024))) char buf0[T::kBufBytes], buf1[T::kBufBytes];
-  __shared__ uint2 sc0[T::kRows], sc1[T::kRows];
+  MX_TILE_LDS(T);
   const int64_t total = (int64_t)mt * nt, per = (total + kXcds - 1) / kXcds;
   const int64_t L = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
   if (blockIdx.x / kXcds >= per || L >= total) return;
@@ -107,16 +107,20 @@ __global__ __launch_bounds__(T::kThreads) void mx_matmul_tile_kernel(const uint8
   const int nl = n - 1 - n0, ml = (int)min(m - 1 - m0, (int64_t)T::TM);
   const MxOperand W{w + (int64_t)n0 * nb * kMxBlockBytes, ws + (int64_t)n0 * nb};
   const MxOperand X{a + m0 * nb * kMxBlockBytes, as + m0 * nb};
-  mx_tile_products<T, WORDS>(W, X, [&](int r) { return min(r, nl); }, [&](int r) { return min(r, ml); }, nb, buf0, buf1,
-                             sc0, sc1, acc);
-  mx_meet();   // the buffers become the waves' output regions
+  mx_tile_products<T, WORDS>(W, X, [&](int r) { return min(r, nl); }, [&](int r) { return min(r, ml); }, nb, MX_TILE_ARGS, acc);
+  mx_meet<0>();   // the buffers becomes the waves' output regions
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t wm0 = m0 + wave % T::WM * T::FM * 32;
   const int wn0 = n0 + wave / T::WM * T::FN * 32;
-  static_assert(T::kBufBytes >= 8192 * T::kWaves, "an output region per wave");
-  mx_tile_rows<T>(buf0 + 8192 * wave, acc, [&](int row, int col, const float* v) {
-    if (wm0 + row < m && wn0 + col < n) mx_put8(out, bf16, wm0 + row, n, wn0 + col, v);
-  });
+  char* region = mx_region<T>(wave, MX_TILE_ARGS);
+  if (bf16)
+    mx_tile_rows_bf16<T>(region, acc, [&](int row, int col, uint4 v) {
+      if (wm0 + row < m && wn0 + col < n) mx_put8(static_cast<uint16_t*>(out), wm0 + row, n, wn0 + col, v);
+    });
+  else
+    mx_tile_rows<T>(region, acc, [&](int row, int col, f32x4 lo, f32x4 hi) {
+      if (wm0 + row < m && wn0 + col < n) mx_put8(static_cast<float*>(out), wm0 + row, n, wn0 + col, lo, hi);
+    });
 }
 
 namespace {
@@ -127,23 +131,23 @@ struct MatmulCall {
   void* out;
   bool bf16;
 };
-template <class T>
+template <class T, bool WORDS>
 void run_tiles(const MatmulCall& c, hipStream_t s) {
   const int mt = (int)((c.m + T::TM - 1) / T::TM), nt = (c.n + T::TN - 1) / T::TN;
   const int64_t per = ((int64_t)mt * nt + kXcds - 1) / kXcds;
   const dim3 grid((unsigned)(per * kXcds)), block(T::kThreads);
-  if (c.nb % 4 == 0)
-    hipLaunchKernelGGL((mx_matmul_tile_kernel<T, true>), grid, block, 0, s, c.a, c.as, c.w, c.ws, c.m, c.n, c.nb, mt, nt,
-                       c.out, c.bf16);
-  else
-    hipLaunchKernelGGL((mx_matmul_tile_kernel<T, false>), grid, block, 0, s, c.a, c.as, c.w, c.ws, c.m, c.n, c.nb, mt,
-                       nt, c.out, c.bf16);
+  hipLaunchKernelGGL((mx_matmul_tile_kernel<T, WORDS>), grid, block, 0, s, c.a, c.as, c.w, c.ws, c.m, c.n, c.nb, mt, nt,
+                     c.out, c.bf16);
 }
 }  // namespace
 
 typedef MxTile<2, 4, 4, 2> MxTile256;   // 256 x 256, 8 waves
 typedef MxTile<2, 2, 2, 2> MxTile128;   // 128 x 128, 4 waves
 
+// The larger tile moves half the bytes through LDS and L2 per product (m 65536, n 2816,
+// k 2048: 243 us against 290), once there are enough of them for most of the CUs
+// (176 tiles of 128, 44 of 256: 8.9 us against 15.8).  Odd scale rows (their fetch takes
+// registers that the larger tile does not have) stay with the smaller one.
 void launch_mx_matmul(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t m, int n, int k,
                       void* out, bool bf16, hipStream_t s) {
   const MatmulCall c{a, as, w, ws, m, n, k / kMxBlock, out, bf16};
@@ -153,10 +157,12 @@ void launch_mx_matmul(const uint8_t* a, const uint8_t* as, const uint8_t* w, con
   else if (m <= 128)
     hipLaunchKernelGGL((mx_matmul_stream_kernel<4, 4>), dim3((unsigned)((m + 63) / 64), nt), dim3(256), 0, s, a, as, w,
                        ws, m, n, c.nb, out, bf16);
-  else if (((m + 255) / 256) * ((n + 255) / 256) < 256)
-    run_tiles<MxTile128>(c, s);
+  else if (mx_words(c.nb) && (m + 255) / 256 * ((n + 255) / 256) >= 192)
+    run_tiles<MxTile256, true>(c, s);
+  else if (mx_words(c.nb))
+    run_tiles<MxTile128, true>(c, s);
   else
-    run_tiles<MxTile256>(c, s);
+    run_tiles<MxTile128, false>(c, s);
 }
 
 }  // namespace clha

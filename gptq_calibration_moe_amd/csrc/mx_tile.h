@@ -1,19 +1,32 @@
 // The inner loop of the MXFP4 products over many rows: a workgroup's tile of
 // WN FN 32 rows of W by WM FM 32 rows of x, both through LDS.
 //
-// WN x WM waves; a wave owns FN x FM products of 32x32 (v_mfma_scale 32x32x64:
-// 1.6 times the rate of the 16x16x128 form, 7.4 against 4.7 PFLOP/s measured on
-// registers alone).  The contraction advances by stages of 8 blocks (256 values,
-// 128 bytes of a row) through two LDS buffers filled by direct global-to-LDS
-// loads, one stage ahead of the products.  A buffer holds 128 bytes per row, the
-// 16-byte block b of row r at slot b ^ (r % 8): a load instruction fills 8 whole
-// rows with 128-byte runs of memory, and the 8 lanes that read together (8 rows,
-// one block each) fall on 8 different slots.  Lane l takes row l % 32 and, in
-// step j of 4, block 4 (l / 32) + j, so the four scale bytes of its row are one
-// LDS word and the instruction's selector picks the byte.
+// WN x WM waves; a wave owns FN x FM products of 32x32 (v_mfma_scale 32x32x64, one
+// per 32 clocks and matrix core).  On registers alone the instruction reaches 9.7
+// PFLOP/s with constant operands and 6.1 with random ones, whose switching holds the
+// clock down: the second is what a product can be measured against.
+// The contraction advances by stages of 8 blocks (256 values) through two LDS
+// buffers filled by direct global-to-LDS loads, one stage ahead of the products.
+// Every load instruction fills 8 whole 128-byte rows: the L2 serves so many requests
+// a clock whatever their size (32 KB a CU took 0.23 us in 128-byte requests, 0.45 to
+// 0.55 us in 64-byte ones, with the whole chip loading).  The 16-byte block b of row r
+// sits at slot b ^ ((r / 2) % 8): 16 consecutive rows of one block then cover all banks.
+// Lane l takes row l % 32 and, in step j of 4, block 4 (l / 32) + j, so its four scale
+// bytes of a stage are one word and the instruction's selector picks the byte.
 //
-// Blocks past the end of the rows (a last stage of nb % 8 blocks): the loads
-// re-read block 0, the W operand is zeroed in registers and both scales are 1.
+// What a step's products need is read from LDS while the step before multiplies,
+// across stages too: the wait for the next stage and its first reads come before the
+// last step's products.
+//
+// Scales are fetched for two stages at a time, 16 bytes of a row per lane (fetched a
+// stage at a time, they were a third of all requests to the L2), into two LDS
+// buffers: directly when rows of scales are whole words and at least 16 bytes (WORDS;
+// an incomplete last pair reads the row's last 16 bytes), else byte-aligned and
+// through registers.
+//
+// Rows of nb blocks, nb not a multiple of 8: in the last stage the blocks past the
+// end re-read the row's first block of it, the W operand is zeroed in registers and
+// both scales are 1.
 #pragma once
 
 #include "mx.h"
@@ -31,18 +44,30 @@ struct MxTile {
   static constexpr int WN = WN_, WM = WM_, FN = FN_, FM = FM_;
   static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves;
   static constexpr int TN = WN * FN * 32, TM = WM * FM * 32, kRows = TN + TM;
-  static constexpr int kLoads = kRows / 8 / kWaves;        // load instructions of a wave per stage
-  static_assert(kRows % (8 * kWaves) == 0 && kRows <= kThreads, "one scale row per thread, whole loads per wave");
-  static_assert(TN % (8 * kLoads) == 0, "a wave's loads come from one operand");
+  static constexpr int kLoads = kRows / 8 / kWaves;        // load instructions of a wave per stage (8 rows each)
+  static constexpr int kWLoads = TN / 8 / kWaves;          // the first of them, from W
+  static constexpr int kScaleRows = kRows / kThreads;      // rows of scales a thread fetches
+  static_assert(TN % (8 * kWaves) == 0 && TM % (8 * kWaves) == 0 && kWaves % 2 == 0, "each load instruction comes from one operand");
   static constexpr int kBufBytes = kRows * kStageBytes;
 };
 
-// This wave's loads in flight and LDS accesses are done, then all waves meet.
+// LDS of a tile in a kernel: two stages' codes and two pairs of stages' scales.
+#define MX_TILE_LDS(T)                                                                     \
+  __shared__ __attribute__((aligned(1024))) char mx_b0[T::kBufBytes], mx_b1[T::kBufBytes]; \
+  __shared__ uint4 mx_s[2 * T::kRows]
+
+#define MX_TILE_ARGS mx_b0, mx_b1, mx_s
+
+inline bool mx_words(int nb) { return nb % 4 == 0 && nb >= 16; }
+
+// This wave's loads but for the last N are done and its LDS accesses too, then all waves meet.
+template <int N>
 __device__ __forceinline__ void mx_meet() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt 0, lgkmcnt 0 (the export count is left at its maximum)
+  asm volatile("" ::: "memory");
+  // the load counter's low four and high two bits, the export count at its maximum, LDS at 0
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (((N >> 4) & 3) << 14));
   __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+  asm volatile("" ::: "memory");
 }
 
 // One operand of a tile: its rows' codes and scales from a base that is the same
@@ -54,153 +79,215 @@ struct MxOperand {
 
 // wrow(r), xrow(r): the row, counted from the operand's base, of the tile's row r
 // (0 .. TN-1, 0 .. TM-1), always one that exists and less than 2^32 bytes from the
-// base.  WORDS: rows of scales are whole 32-bit words (nb a multiple of 4).
+// base.  The buffers are separate arrays so that the compiler can tell a stage being
+// loaded from one being read.  WORDS: nb is a multiple of 4, at least 16.
 // acc[FN][FM] += the tile's products over nb blocks.
 template <class T, bool WORDS, class WRow, class XRow>
 __device__ __forceinline__ void mx_tile_products(const MxOperand& W, const MxOperand& X, WRow&& wrow_of, XRow&& xrow_of,
-                                                 int nb, char* buf0, char* buf1, uint2* sc0, uint2* sc1,
+                                                 int nb, char* b0, char* b1, uint4* sc,
                                                  f32x16 (&acc)[T::FN][T::FM]) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave / T::WM, wm = wave % T::WM;
-  const int stages = (nb + kStageBlocks - 1) / kStageBlocks;
-  const int piece = (lane & 7) ^ (lane >> 3);   // the block that lands in slot lane % 8 of row lane / 8
-  const int first = wave * T::kLoads * 8;       // this wave's first tile row of the loads
-  const uint8_t* cbase = first < T::TN ? W.codes : X.codes;
+  const int stages = (nb + kStageBlocks - 1) / kStageBlocks, full = nb / kStageBlocks;
+  // load i of this wave fills tile rows 8 (kWaves i + wave) .. + 7; the block that lands in slot lane % 8 of row lane / 8
+  const int piece = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
   uint32_t src[T::kLoads];
 #pragma unroll
   for (int i = 0; i < T::kLoads; ++i) {
-    const int r = first + 8 * i + (lane >> 3);
-    src[i] = (uint32_t)(first < T::TN ? wrow_of(r) : xrow_of(r - T::TN)) * (uint32_t)(nb * kMxBlockBytes) +
+    const int r = 8 * (T::kWaves * i + wave) + (lane >> 3);
+    src[i] = (uint32_t)(i < T::kWLoads ? wrow_of(r) : xrow_of(r - T::TN)) * (uint32_t)(nb * kMxBlockBytes) +
              piece * kMxBlockBytes;
   }
-  // one row of scales per thread (a wave's rows come from one operand)
-  static_assert(T::TN % 64 == 0, "whole waves");
-  const bool swave_w = wave * 64 < T::TN;
-  const uint8_t* sbase = swave_w ? W.scales : X.scales;
-  const int sr = min((int)threadIdx.x, T::kRows - 1);
-  const uint32_t soff = (uint32_t)(swave_w ? wrow_of(sr) : xrow_of(sr - T::TN)) * (uint32_t)nb;
+  // scale row i of this thread is tile row kThreads i + threadIdx.x (a wave's rows come from one operand)
+  static_assert(T::TN % 64 == 0 && T::kRows % T::kThreads == 0, "whole waves of scale rows");
+  uint32_t ssrc[T::kScaleRows];
+#pragma unroll
+  for (int i = 0; i < T::kScaleRows; ++i) {
+    const int r0 = T::kThreads * i + 64 * wave;
+    ssrc[i] = (uint32_t)(r0 < T::TN ? wrow_of(r0 + lane) : xrow_of(r0 + lane - T::TN)) * (uint32_t)nb;
+  }
 
-  auto issue = [&](int s, char* buf) {
-    const int left = nb - s * kStageBlocks;
-    const uint8_t* base = cbase + (int64_t)s * kStageBytes;
-    asm volatile("" : "+s"(base));   // a scalar base per stage: no 64-bit address per load lives across stages
-    const uint32_t back = piece < left ? 0u : (uint32_t)(piece * kMxBlockBytes);
+  // Loads of a stage; past the last one it re-reads that (no branch in the loop, and
+  // the buffer is not read again).
+  auto issue = [&](int s, char* b) {
+    s = min(s, stages - 1);
+    const uint8_t *wb = W.codes + (int64_t)s * kStageBytes, *xb = X.codes + (int64_t)s * kStageBytes;
+    asm volatile("" : "+s"(wb), "+s"(xb));   // scalar bases: no 64-bit address per load lives across stages
+    const uint32_t back = piece < nb - s * kStageBlocks ? 0u : (uint32_t)(piece * kMxBlockBytes);
 #pragma unroll
     for (int i = 0; i < T::kLoads; ++i)
-      __builtin_amdgcn_global_load_lds((mx_glb_ptr)(base + (src[i] - back)),
-                                       (mx_lds_ptr)(buf + (first + 8 * i) * kStageBytes), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((mx_glb_ptr)((i < T::kWLoads ? wb : xb) + (src[i] - back)),
+                                       (mx_lds_ptr)(b + 8 * (T::kWaves * i + wave) * kStageBytes), 16, 0, 0);
   };
+  // WORDS: the scales of stages s and s + 1 into `to`; they start at word first_word(s) of a row's four.
+  auto issue_scales = [&](int s, uint4* to) {
+    const int at = min(s * kStageBlocks, nb - 16);
+    const uint8_t *ws = W.scales + at, *xs = X.scales + at;
+    asm volatile("" : "+s"(ws), "+s"(xs));
+#pragma unroll
+    for (int i = 0; i < T::kScaleRows; ++i) {
+      const int r0 = T::kThreads * i + 64 * wave;
+      __builtin_amdgcn_global_load_lds((mx_glb_ptr)((r0 < T::TN ? ws : xs) + ssrc[i]), (mx_lds_ptr)(to + r0), 16, 0, 0);
+    }
+  };
+  auto first_word = [&](int s) {
+    if constexpr (WORDS) return (s * kStageBlocks - min(s * kStageBlocks, nb - 16)) / 4;
+    return 0;
+  };
+  // Otherwise: the same for this thread's rows, through registers (bytes past the end: 1).
+  uint4 sv[T::kScaleRows];
   auto load_scales = [&](int s) {
     const int left = nb - s * kStageBlocks;
-    const uint8_t* p = sbase + s * kStageBlocks + soff;
-    uint2 v;
-    if constexpr (WORDS) {
-      v.x = reinterpret_cast<const uint32_t*>(p)[0];
-      v.y = reinterpret_cast<const uint32_t*>(p)[left > 4 ? 1 : 0];   // replaced when it is published
-    } else {
-      uint32_t w[8];
+    if (left <= 0) return;
 #pragma unroll
-      for (int b = 0; b < 8; ++b) w[b] = p[b < left ? b : 0];
-#pragma unroll
-      for (int b = 0; b < 8; ++b) w[b] = b < left ? w[b] : (uint32_t)kMxOne;
-      v.x = w[0] | (w[1] << 8) | (w[2] << 16) | (w[3] << 24);
-      v.y = w[4] | (w[5] << 8) | (w[6] << 16) | (w[7] << 24);
+    for (int i = 0; i < T::kScaleRows; ++i) {
+      const uint8_t* p = (T::kThreads * i + 64 * wave < T::TN ? W.scales : X.scales) + s * kStageBlocks + ssrc[i];
+      if (left >= 16) {
+        __builtin_memcpy(&sv[i], p, 16);
+      } else {
+        uint64_t lo = 0x7f7f7f7f7f7f7f7full, hi = lo;
+#pragma unroll 1
+        for (int k = 0; k < left; ++k) {
+          uint64_t& v = k < 8 ? lo : hi;
+          const int at = 8 * (k & 7);
+          v = (v & ~(0xffull << at)) | ((uint64_t)p[k] << at);
+        }
+        sv[i] = make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+      }
     }
-    return v;
+  };
+  auto store_scales = [&](uint4* to) {
+#pragma unroll
+    for (int i = 0; i < T::kScaleRows; ++i) to[T::kThreads * i + threadIdx.x] = sv[i];
   };
   // lane's first W and x rows in the tile, and its block slot of step 0
   const int r = lane & 31, g = lane >> 5;
   const int wrow = wn * T::FN * 32 + r, xrow = T::TN + wm * T::FM * 32 + r;
-  const int slot0 = (4 * g) ^ (r & 7);
-  // One stage's products; left < 8 (TAIL): blocks left .. 7 of the stage are past the end.
-  auto products = [&](const char* buf, const uint2* sc, auto tail_, int left) {
-    constexpr bool TAIL = decltype(tail_)::value;
-    int sw[T::FN], sx[T::FM];
-    i32x4 w[2][T::FN], x[2][T::FM];
+  const int slot0 = (4 * g) ^ ((r >> 1) & 7);
+  // Fragments of two steps, and the scale words of two stages.
+  i32x4 w[2][T::FN], x[2][T::FM];
+  int cw[2][T::FN], cx[2][T::FM];
+  // Scale words of the stage that is the half-th of its two.
+  auto fetch_scales = [&](const uint4* scales, int first, int half) {
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(scales) + first + 2 * half + g;
 #pragma unroll
-    for (int a = 0; a < T::FN; ++a) sw[a] = reinterpret_cast<const int*>(sc + wrow + 32 * a)[g];
+    for (int a = 0; a < T::FN; ++a) cw[half][a] = (int)words[4 * (wrow + 32 * a)];
 #pragma unroll
-    for (int b = 0; b < T::FM; ++b) sx[b] = reinterpret_cast<const int*>(sc + xrow + 32 * b)[g];
+    for (int b = 0; b < T::FM; ++b) cx[half][b] = (int)words[4 * (xrow + 32 * b)];
+  };
+  auto fetch = [&](const char* stage, int j) {
     int wat = wrow * kStageBytes + slot0 * kMxBlockBytes, xat = xrow * kStageBytes + slot0 * kMxBlockBytes;
-    asm volatile("" : "+v"(wat), "+v"(xat));   // formed here: eight addresses across stages would spill
-    auto fetch = [&](int j) {
-      asm volatile("" ::: "memory");   // reads stay behind this point (four steps' fragments would not fit)
-      // rows are 128 bytes apart: step j's slot is a flip of address bits 4 and 5
-      const char* wp = buf + (wat ^ (j * kMxBlockBytes));
-      const char* xp = buf + (xat ^ (j * kMxBlockBytes));
+    asm volatile("" : "+v"(wat), "+v"(xat)::"memory");   // formed here, not kept per buffer and step
+    // rows are 128 bytes apart: step j's slot is a flip of address bits 4 and 5
+    const char* wp = stage + (wat ^ (j * kMxBlockBytes));
+    const char* xp = stage + (xat ^ (j * kMxBlockBytes));
 #pragma unroll
-      for (int a = 0; a < T::FN; ++a) w[j & 1][a] = *reinterpret_cast<const i32x4*>(wp + 32 * a * kStageBytes);
+    for (int a = 0; a < T::FN; ++a) w[j & 1][a] = *reinterpret_cast<const i32x4*>(wp + 32 * a * kStageBytes);
 #pragma unroll
-      for (int b = 0; b < T::FM; ++b) x[j & 1][b] = *reinterpret_cast<const i32x4*>(xp + 32 * b * kStageBytes);
-      if constexpr (TAIL) {
-        const int keep = 4 * g + j < left ? -1 : 0;
+    for (int b = 0; b < T::FM; ++b) x[j & 1][b] = *reinterpret_cast<const i32x4*>(xp + 32 * b * kStageBytes);
+  };
+  auto multiply = [&](auto j_, int half) {
+    constexpr int j = decltype(j_)::value;
 #pragma unroll
-        for (int a = 0; a < T::FN; ++a) w[j & 1][a] &= i32x4{keep, keep, keep, keep};
-      }
-    };
-    auto multiply = [&](auto j_) {
-      constexpr int j = decltype(j_)::value;
+    for (int a = 0; a < T::FN; ++a)
 #pragma unroll
-      for (int a = 0; a < T::FN; ++a)
-#pragma unroll
-        for (int b = 0; b < T::FM; ++b) acc[a][b] = mx_mfma32<j>(w[j & 1][a], x[j & 1][b], acc[a][b], sw[a], sx[b]);
-    };
-    // a step's fragments are read ahead of the products of the step before
-    auto paced = [&] {
-      __builtin_amdgcn_sched_group_barrier(0x100, T::FN + T::FM, 0);   // LDS reads
-      __builtin_amdgcn_sched_group_barrier(0x008, T::FN * T::FM, 0);   // matrix instructions
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    fetch(0);
+      for (int b = 0; b < T::FM; ++b)
+        acc[a][b] = mx_mfma32<j>(w[j & 1][a], x[j & 1][b], acc[a][b], cw[half][a], cx[half][b]);
+  };
+  const std::integral_constant<int, 0> J0;
+  const std::integral_constant<int, 1> J1;
+  const std::integral_constant<int, 2> J2;
+  const std::integral_constant<int, 3> J3;
+  // A whole stage in `here`, the half-th of its two, whose step 0 and scales are
+  // fetched.  Before its last step: the next stage has arrived and every wave has
+  // read this one, so the stage after next starts into its place; with the first of
+  // two stages go the next two's scales, which the second one publishes.
+  auto turn = [&](int s, char* here, const char* there, const uint4* scales, uint4* other, auto half_) {
+    constexpr int half = decltype(half_)::value;
+    fetch(here, 1);
     __builtin_amdgcn_sched_barrier(0);
-    fetch(1);
-    multiply(std::integral_constant<int, 0>());
-    paced();
-    fetch(2);
-    multiply(std::integral_constant<int, 1>());
-    paced();
-    fetch(3);
-    multiply(std::integral_constant<int, 2>());
-    paced();
-    multiply(std::integral_constant<int, 3>());
+    multiply(J0, half);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(here, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(J1, half);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(here, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(J2, half);
+    if constexpr (half == 1 && !WORDS) store_scales(other);
+    mx_meet<0>();
+    if constexpr (half == 0) fetch_scales(scales, first_word(s), 1);
+    else fetch_scales(other, first_word(s + 1), 0);
+    fetch(there, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    issue(s + 2, here);
+    if constexpr (half == 0 && WORDS) issue_scales(s + 2, other);
+    if constexpr (half == 0 && !WORDS) load_scales(s + 2);
+    multiply(J3, half);
+    __builtin_amdgcn_sched_barrier(0);
   };
-  const int full = nb / kStageBlocks;
-  uint2 sv = load_scales(0);
-  issue(0, buf0);
-  // Publishes stage s and starts the next one into `nxt`; past the last stage it
-  // re-reads that one (no branch in the loop, and the buffer is not read again).
-  auto begin = [&](int s, char* nxt, uint2* sc) {
-    if (WORDS && nb - s * kStageBlocks <= 4) sv.y = 0x7f7f7f7fu;
-    if (T::kRows == T::kThreads || (int)threadIdx.x < T::kRows) sc[threadIdx.x] = sv;
-    mx_meet();
-    const int next = min(s + 1, stages - 1);
-    sv = load_scales(next);
-    issue(next, nxt);
-  };
-  int s = 0;
+  if constexpr (WORDS) {
+    issue_scales(0, sc);
+  } else {
+    load_scales(0);
+    store_scales(sc);
+  }
+  issue(0, b0);
+  mx_meet<0>();
+  fetch_scales(sc, first_word(0), 0);
+  fetch(b0, 0);
+  issue(1, b1);
+  int s = 0, at = 0;   // the scales of stages s and s + 1 are at sc + at
 #pragma unroll 1
-  for (; s + 1 < full; s += 2) {
-    begin(s, buf1, sc0);
-    products(buf0, sc0, std::false_type(), kStageBlocks);
-    begin(s + 1, buf0, sc1);
-    products(buf1, sc1, std::false_type(), kStageBlocks);
+  for (; s + 2 <= full; s += 2) {
+    turn(s, b0, b1, sc + at, sc + (T::kRows - at), J0);
+    turn(s + 1, b1, b0, sc + at, sc + (T::kRows - at), J1);
+    at = T::kRows - at;
   }
-  if (s < full) {   // s is even
-    begin(s, buf1, sc0);
-    products(buf0, sc0, std::false_type(), kStageBlocks);
-  }
-  if (full < stages) {
-    char *cur = full & 1 ? buf1 : buf0, *other = full & 1 ? buf0 : buf1;
-    uint2* sc = full & 1 ? sc1 : sc0;
-    begin(full, other, sc);
-    products(cur, sc, std::true_type(), nb - full * kStageBlocks);
+  if (s < full) turn(s, b0, b1, sc + at, sc + (T::kRows - at), J0);
+  if (full < stages) {   // blocks left .. 7 of the last stage are past the end
+    const int half = full & 1, left = nb - full * kStageBlocks;
+    mx_meet<0>();
+    const char* here = half ? b1 : b0;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(sc + at) + first_word(s) + 2 * half + (4 * g < left ? g : 0);
+    const int none = 4 * g < left ? 0 : -1;   // no block of this lane is left
+    const int one = 0x7f7f7f7f;
+#pragma unroll
+    for (int a = 0; a < T::FN; ++a) cw[0][a] = none ? one : (int)words[4 * (wrow + 32 * a)];
+#pragma unroll
+    for (int b = 0; b < T::FM; ++b) cx[0][b] = none ? one : (int)words[4 * (xrow + 32 * b)];
+    auto masked = [&](int j) {
+      fetch(here, j);
+      const int keep = 4 * g + j < left ? -1 : 0;
+#pragma unroll
+      for (int a = 0; a < T::FN; ++a) w[j & 1][a] &= i32x4{keep, keep, keep, keep};
+    };
+    masked(0);
+    masked(1);
+    multiply(J0, 0);
+    multiply(J1, 0);
+    masked(2);
+    masked(3);
+    multiply(J2, 0);
+    multiply(J3, 0);
   }
 }
 
-// A wave's results as rows of x: 32 rows of 64 columns at a time through an 8 KB
-// LDS region of the wave's own (16-byte column group c of row i at c ^ (i % 16)),
-// so that rows leave as whole cache lines.  put(row, col, v): eight fp32 results
-// of consecutive columns col.. (0 .. FN*32-1 of the wave) of its row (0 .. FM*32-1).
+// The 8 KB region of a wave in the two buffers.
+template <class T>
+__device__ __forceinline__ char* mx_region(int wave, char* b0, char* b1, uint4*) {
+  constexpr int per = T::kBufBytes / 8192;
+  static_assert(2 * per >= T::kWaves, "an output region per wave");
+  return wave < per ? b0 + 8192 * wave : b1 + 8192 * (wave - per);
+}
+
+// A wave's results as rows of x, through an 8 KB LDS region of its own so that rows
+// leave as whole cache lines.
+
+// fp32, 32 rows of 64 columns at a time (16-byte group c of row i at c ^ (i % 16)).
+// put(row, col, v): eight results of consecutive columns col.. (0 .. FN*32-1 of the
+// wave) of its row (0 .. FM*32-1).
 template <class T, class Put>
 __device__ __forceinline__ void mx_tile_rows(char* region, const f32x16 (&acc)[T::FN][T::FM], Put&& put) {
   const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
@@ -222,11 +309,39 @@ __device__ __forceinline__ void mx_tile_rows(char* region, const f32x16 (&acc)[T
       for (int i = 0; i < 4; ++i) {
         const int row = 8 * i + (lane >> 3), c = 2 * (lane & 7);
         const f32x4 lo = box[row * 16 + (c ^ (row & 15))], hi = box[row * 16 + ((c + 1) ^ (row & 15))];
-        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        put(32 * b + row, 32 * a + 8 * (lane & 7), v);
+        put(32 * b + row, 32 * a + 8 * (lane & 7), lo, hi);
       }
       __builtin_amdgcn_wave_barrier();
     }
+}
+
+// bf16, 32 rows at a time: rounded before they go through LDS, which halves its
+// traffic (the epilogue's bound).  put(row, col, q): eight results.
+template <class T, class Put>
+__device__ __forceinline__ void mx_tile_rows_bf16(char* region, const f32x16 (&acc)[T::FN][T::FM], Put&& put) {
+  constexpr int kGroups = 4 * T::FN;   // of 16 bytes in a row
+  static_assert(32 * kGroups * 16 <= 8192 && (kGroups & (kGroups - 1)) == 0, "rows in the region, power of two");
+  const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
+  uint2* half = reinterpret_cast<uint2*>(region);
+  const uint4* whole = reinterpret_cast<const uint4*>(region);
+#pragma unroll
+  for (int b = 0; b < T::FM; ++b) {
+#pragma unroll
+    for (int a = 0; a < T::FN; ++a)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x16& v = acc[a][b];
+        half[2 * (r * kGroups + ((4 * a + q) ^ (r & (kGroups - 1)))) + g] =
+            make_uint2(mx_bf16_pair(v[4 * q], v[4 * q + 1]), mx_bf16_pair(v[4 * q + 2], v[4 * q + 3]));
+      }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int i = 0; i < kGroups / 2; ++i) {
+      const int row = i * (64 / kGroups) + lane / kGroups, c = lane % kGroups;
+      put(32 * b + row, 8 * c, whole[row * kGroups + (c ^ (row & (kGroups - 1)))]);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
 }
 
 }  // namespace clha

@@ -452,6 +452,7 @@ CLHA_API size_t clha_mx_experts_workspace_bytes(const clha_ctx* ctx, int64_t n_t
  *         experts' with weight 1 (fp32); one rounding to the output type.
  * MX(.) is clha_mx_quantize.
  *   x        device, bf16 bits [n_tokens][d]; n_tokens 0..max_tokens, at most 2^27 / (K + n_shared)
+ *            and 2^33 / d
  *   topk     device, int32 [n_tokens][K]; an id outside 0..E-1 stands for no expert and adds
  *            nothing; the same expert twice counts twice
  *   weights  device, float [n_tokens][K]
