@@ -13,6 +13,7 @@ Names follow the C entry points: ``Context.collect_hessians`` calls
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -161,6 +162,17 @@ def _bits16(t: torch.Tensor) -> torch.Tensor:
     if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
         return t
     raise TypeError(f"expected bf16 activations, got {t.dtype}")
+
+
+def _ok(t, dtype, device, shape) -> bool:
+    """The usual case of _check_dev, which names what is wrong otherwise."""
+    return (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous())
+
+
+@functools.lru_cache(maxsize=256)
+def _route_desc_of(*args) -> RouteDesc:
+    return route_desc(*args)
 
 
 class Context:
@@ -480,8 +492,8 @@ class Context:
     # These calls run on `stream`, or on the current stream of the context's device; outputs and
     # workspaces that they make belong to that stream.
 
-    def _on(self, stream):
-        return torch.cuda.current_stream(self.device) if stream is None else stream
+    def _raw_stream(self, stream) -> int:
+        return torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else stream.cuda_stream
 
     def _new(self, shape, dtype, stream):
         if stream is None:
@@ -489,92 +501,105 @@ class Context:
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
+    def _want(self, name, t, dtype, shape):
+        if not _ok(t, dtype, self.device, shape):
+            _check_dev(name, t, dtype, shape, self.device)
+
+    def _out(self, name, t, dtype, shape, stream):
+        """The given output, checked, or a new one."""
+        if t is None:
+            return self._new(shape, dtype, stream)
+        self._want(name, t, dtype, shape)
+        return t
+
     def route(self, logits: torch.Tensor, score: str = "softmax", bias: Optional[torch.Tensor] = None,
               groups: int = 1, top_groups: int = 1, group_score: str = "max", renormalize: bool = True,
               scale: float = 1.0, topk_out: Optional[torch.Tensor] = None,
               weights_out: Optional[torch.Tensor] = None, stream=None):
         """clha_route: (topk int32 [n, K], weights float32 [n, K]) of logits [n, E]."""
         n = logits.shape[0]
-        _check_dev("logits", logits, torch.float32, (n, self.n_routed), self.device)
+        self._want("logits", logits, torch.float32, (n, self.n_routed))
         if bias is not None:
-            _check_dev("bias", bias, torch.float32, (self.n_routed,), self.device)
-        desc = route_desc(score, groups, top_groups, group_score, renormalize, scale)
-        topk = self._new((n, self.top_k), torch.int32, stream) if topk_out is None else topk_out
-        weights = self._new((n, self.top_k), torch.float32, stream) if weights_out is None else weights_out
-        if topk_out is not None:
-            _check_dev("topk_out", topk, torch.int32, (n, self.top_k), self.device)
-        if weights_out is not None:
-            _check_dev("weights_out", weights, torch.float32, (n, self.top_k), self.device)
-        self._raise(lib.clha_route(self._h, C.byref(desc), n, _ptr(logits), _ptr(bias), _ptr(topk), _ptr(weights),
-                                   _stream(self._on(stream))))
+            self._want("bias", bias, torch.float32, (self.n_routed,))
+        desc = _route_desc_of(score, groups, top_groups, group_score, renormalize, scale)
+        shape = (n, self.top_k)
+        topk = self._out("topk_out", topk_out, torch.int32, shape, stream)
+        weights = self._out("weights_out", weights_out, torch.float32, shape, stream)
+        st = lib.clha_route(self._h, desc, n, logits.data_ptr(), None if bias is None else bias.data_ptr(),
+                            topk.data_ptr(), weights.data_ptr(), self._raw_stream(stream))
+        if st:
+            self._raise(st)
         return topk, weights
 
     def mx_quantize(self, x: torch.Tensor, codes_out: Optional[torch.Tensor] = None,
                     scales_out: Optional[torch.Tensor] = None, stream=None):
         """clha_mx_quantize: (codes uint8 [..., cols/2], scales uint8 [..., cols/32]) of a contiguous
         fp32 or bf16 tensor, or of a matrix whose rows are contiguous."""
-        cols = x.shape[-1]
-        rows = x.numel() // cols if cols else 0
+        if not isinstance(x, torch.Tensor):
+            raise TypeError("x must be a torch tensor")
+        *lead, cols = x.shape
         ld = cols
-        if x.dim() == 2 and x.stride(1) == 1 and rows > 1:
+        if not x.is_contiguous() and x.dim() == 2 and x.stride(1) == 1:
             ld = x.stride(0)
             _check_dev("x", x[0], (torch.float32, torch.bfloat16), None, self.device)
-        else:
+        elif not (x.is_contiguous() and x.device == self.device and x.dtype in (torch.float32, torch.bfloat16)):
             _check_dev("x", x, (torch.float32, torch.bfloat16), None, self.device)
         if cols % 32:
             raise ValueError("the last dimension of x must be a multiple of 32")
-        shape, sshape = (*x.shape[:-1], cols // 2), (*x.shape[:-1], cols // 32)
-        codes = self._new(shape, torch.uint8, stream) if codes_out is None else codes_out
-        scales = self._new(sshape, torch.uint8, stream) if scales_out is None else scales_out
-        if codes_out is not None:
-            _check_dev("codes_out", codes, torch.uint8, shape, self.device)
-        if scales_out is not None:
-            _check_dev("scales_out", scales, torch.uint8, sshape, self.device)
-        self._raise(lib.clha_mx_quantize(self._h, rows, cols, _ptr(x), BF16 if x.dtype == torch.bfloat16 else F32,
-                                         ld, _ptr(codes), _ptr(scales), _stream(self._on(stream))))
+        codes = self._out("codes_out", codes_out, torch.uint8, (*lead, cols // 2), stream)
+        scales = self._out("scales_out", scales_out, torch.uint8, (*lead, cols // 32), stream)
+        st = lib.clha_mx_quantize(self._h, x.numel() // cols if cols else 0, cols, x.data_ptr(),
+                                  BF16 if x.dtype is torch.bfloat16 else F32, ld, codes.data_ptr(), scales.data_ptr(),
+                                  self._raw_stream(stream))
+        if st:
+            self._raise(st)
         return codes, scales
 
-    def _check_mx(self, name, codes, scales):
-        _check_dev(name, codes, torch.uint8, None, self.device)
+    def _want_mx(self, name, codes, scales):
+        if not (type(codes) is torch.Tensor and codes.dtype is torch.uint8 and codes.device == self.device
+                and codes.is_contiguous()):
+            _check_dev(name, codes, torch.uint8, None, self.device)
         if codes.dim() < 1 or codes.shape[-1] % 16:
             raise ValueError(f"{name} needs rows of a multiple of 32 values (16 bytes)")
-        _check_dev(name + "_scales", scales, torch.uint8, (*codes.shape[:-1], codes.shape[-1] // 16), self.device)
+        *lead, half = codes.shape
+        self._want(name + "_scales", scales, torch.uint8, (*lead, half // 16))
+
+    @staticmethod
+    def _out_type(dtype):
+        if dtype is torch.bfloat16:
+            return BF16
+        if dtype is torch.float32:
+            return F32
+        raise TypeError(f"results are bfloat16 or float32, not {dtype}")
 
     def mx_dequantize(self, codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """clha_mx_dequantize: the values [..., cols] in fp32 or bf16."""
-        self._check_mx("codes", codes, scales)
-        cols = 2 * codes.shape[-1]
-        shape = (*codes.shape[:-1], cols)
+        self._want_mx("codes", codes, scales)
+        *lead, half = codes.shape
         dt = self._out_type(dtype)
-        y = self._new(shape, dtype, stream) if out is None else out
-        if out is not None:
-            _check_dev("out", y, dtype, shape, self.device)
-        self._raise(lib.clha_mx_dequantize(self._h, codes.numel() // (cols // 2) if cols else 0, cols, _ptr(codes),
-                                           _ptr(scales), _ptr(y), dt, _stream(self._on(stream))))
+        y = self._out("out", out, dtype, (*lead, 2 * half), stream)
+        st = lib.clha_mx_dequantize(self._h, codes.numel() // half if half else 0, 2 * half, codes.data_ptr(),
+                                    scales.data_ptr(), y.data_ptr(), dt, self._raw_stream(stream))
+        if st:
+            self._raise(st)
         return y
-
-    @staticmethod
-    def _out_type(dtype):
-        if dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError(f"results are bfloat16 or float32, not {dtype}")
-        return BF16 if dtype == torch.bfloat16 else F32
 
     def mx_matmul(self, a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
                   dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
         """clha_mx_matmul: a [m, k] times w [n, k] transposed, both MXFP4, in fp32 or bf16 [m, n]."""
-        self._check_mx("a", a, a_scales)
-        self._check_mx("w", w, w_scales)
+        self._want_mx("a", a, a_scales)
+        self._want_mx("w", w, w_scales)
         if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
             raise ValueError(f"a {tuple(a.shape)} and w {tuple(w.shape)} must be matrices of equal row length")
-        m, n, k = a.shape[0], w.shape[0], 2 * a.shape[1]
+        (m, half), n = a.shape, w.shape[0]
         dt = self._out_type(dtype)
-        y = self._new((m, n), dtype, stream) if out is None else out
-        if out is not None:
-            _check_dev("out", y, dtype, (m, n), self.device)
-        self._raise(lib.clha_mx_matmul(self._h, m, n, k, _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(y),
-                                       dt, _stream(self._on(stream))))
+        y = self._out("out", out, dtype, (m, n), stream)
+        st = lib.clha_mx_matmul(self._h, m, n, 2 * half, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(),
+                                w_scales.data_ptr(), y.data_ptr(), dt, self._raw_stream(stream))
+        if st:
+            self._raise(st)
         return y
 
     def mx_experts_workspace_bytes(self, n_tokens: int, f: int) -> int:
@@ -585,28 +610,30 @@ class Context:
                    dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """clha_mx_experts: x [n, d] bf16 through the block's MXFP4 experts, E routed ones chosen by
-        (topk, weights) [n, K] and the shared ones; wgu [E + n_shared, 2f, d], wd [E + n_shared, d, f]."""
+        (topk, weights) [n, K] and the shared ones; wgu [E + n_shared, 2f, d], wd [E + n_shared, d, f].
+        Without a workspace each call takes its own."""
         n, d, experts = x.shape[0], self.d, self.n_routed + self.n_shared
         f = 2 * wd.shape[-1]
-        _check_dev("x", x, (torch.bfloat16, torch.int16, torch.uint16), (n, d), self.device)
-        _check_dev("topk", topk, torch.int32, (n, self.top_k), self.device)
-        _check_dev("weights", weights, torch.float32, (n, self.top_k), self.device)
-        _check_dev("wgu", wgu, torch.uint8, (experts, 2 * f, d // 2), self.device)
-        _check_dev("wgu_scales", wgu_scales, torch.uint8, (experts, 2 * f, d // 32), self.device)
-        _check_dev("wd", wd, torch.uint8, (experts, d, f // 2), self.device)
-        _check_dev("wd_scales", wd_scales, torch.uint8, (experts, d, f // 32), self.device)
+        if not _ok(x, torch.bfloat16, self.device, (n, d)):
+            _check_dev("x", x, (torch.bfloat16, torch.int16, torch.uint16), (n, d), self.device)
+        self._want("topk", topk, torch.int32, (n, self.top_k))
+        self._want("weights", weights, torch.float32, (n, self.top_k))
+        self._want("wgu", wgu, torch.uint8, (experts, 2 * f, d // 2))
+        self._want("wgu_scales", wgu_scales, torch.uint8, (experts, 2 * f, d // 32))
+        self._want("wd", wd, torch.uint8, (experts, d, f // 2))
+        self._want("wd_scales", wd_scales, torch.uint8, (experts, d, f // 32))
         dt = self._out_type(dtype)
-        y = self._new((n, d), dtype, stream) if out is None else out
-        if out is not None:
-            _check_dev("out", y, dtype, (n, d), self.device)
+        y = self._out("out", out, dtype, (n, d), stream)
         ws = workspace
         if ws is None:
-            ws = self._new((max(self.mx_experts_workspace_bytes(n, f), 256),), torch.uint8, stream)
+            ws = self._new((max(lib.clha_mx_experts_workspace_bytes(self._h, n, f), 256),), torch.uint8, stream)
         else:
             _check_dev("workspace", ws, torch.uint8, None, self.device)
-        self._raise(lib.clha_mx_experts(self._h, n, f, _ptr(x), _ptr(topk), _ptr(weights), _ptr(wgu),
-                                        _ptr(wgu_scales), _ptr(wd), _ptr(wd_scales), _ptr(y), dt, _ptr(ws),
-                                        ws.numel(), _stream(self._on(stream))))
+        st = lib.clha_mx_experts(self._h, n, f, x.data_ptr(), topk.data_ptr(), weights.data_ptr(), wgu.data_ptr(),
+                                 wgu_scales.data_ptr(), wd.data_ptr(), wd_scales.data_ptr(), y.data_ptr(), dt,
+                                 ws.data_ptr(), ws.numel(), self._raw_stream(stream))
+        if st:
+            self._raise(st)
         return y
 
     def set_timing(self, enable: bool):

@@ -19,82 +19,136 @@
 namespace clha {
 
 // ------------------------------------------------------------------ plan
-// Counting sort of the routed pairs by slot, kPlanPairs pairs per workgroup.
-constexpr int kPlanPairs = 4096;
+// Counting sort of the routed pairs by slot and the tiles: (slot, first position,
+// rows) with at most `rows` positions each.  Up to kPlanPairs pairs one workgroup does
+// all of it, beside the workgroups that quantize x in the same launch; beyond that
+// three launches with kPlanPairs pairs per workgroup.
+constexpr int kPlanPairs = 1024;
+constexpr int kPlanThreads = 512;
 
-__global__ __launch_bounds__(256) void experts_count_kernel(const int32_t* __restrict__ topk, int64_t pairs, int E,
-                                                            int32_t* __restrict__ blockcounts) {
-  __shared__ int32_t cnt[kMaxExperts];
-  for (int e = threadIdx.x; e < E; e += 256) cnt[e] = 0;
+// The exclusive sum of v over the workgroup's threads; *total the whole.
+__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* wave_sum, int32_t* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int32_t y = __shfl_up(x, o);
+    if (lane >= o) x += y;
+  }
   __syncthreads();
-  const int64_t base = (int64_t)blockIdx.x * kPlanPairs;
-  for (int i = threadIdx.x; i < kPlanPairs; i += 256) {
-    if (base + i >= pairs) break;
-    const int e = topk[base + i];
+  if (lane == 63) wave_sum[wave] = x;
+  __syncthreads();
+  int32_t base = 0, all = 0;
+  for (int w = 0; w < kPlanThreads / 64; ++w) {
+    if (w < wave) base += wave_sum[w];
+    all += wave_sum[w];
+  }
+  *total = all;
+  return base + x - v;
+}
+
+// Offsets and tiles of the slots, whose routed counts are in cnt[] (LDS): thread e
+// has slot e (slots <= kPlanThreads).  first[e] becomes the slot's first position.
+__device__ __forceinline__ void plan_tiles(const int32_t* cnt, int32_t* first, int32_t* wave_sum, int E, int slots,
+                                           int32_t n, int32_t pairs, int rows, int32_t* __restrict__ tiles,
+                                           int32_t* __restrict__ n_tiles) {
+  const int e = threadIdx.x;
+  const int32_t mine = e < E ? cnt[e] : e < slots ? n : 0;
+  int32_t total;
+  const int32_t off = block_scan(e < E ? mine : 0, wave_sum, &total);
+  const int32_t pos = e < E ? off : pairs + (e - E) * n;
+  const int32_t tile0 = block_scan((mine + rows - 1) / rows, wave_sum, &total);
+  if (e < E) first[e] = pos;
+  if (threadIdx.x == 0) *n_tiles = total;
+  for (int i = 0; i * rows < mine; ++i) {
+    int32_t* d = tiles + 3 * (int64_t)(tile0 + i);
+    d[0] = e;
+    d[1] = pos + i * rows;
+    d[2] = min(rows, mine - i * rows);
+  }
+  __syncthreads();
+}
+static_assert(kMaxExpertSlots <= kPlanThreads, "a thread per slot");
+
+__device__ __forceinline__ void count_pairs(const int32_t* __restrict__ topk, int64_t from, int64_t to, int E,
+                                            int32_t* cnt) {
+  for (int e = threadIdx.x; e < E; e += kPlanThreads) cnt[e] = 0;
+  __syncthreads();
+  for (int64_t i = from + threadIdx.x; i < to; i += kPlanThreads) {
+    const int e = topk[i];
     if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += 256) blockcounts[(int64_t)blockIdx.x * E + e] = cnt[e];
 }
 
-// One workgroup: each block's base within its slot, the slots' offsets, and the
-// tiles: (slot, first position, rows) with at most `rows` positions each.
-__global__ __launch_bounds__(1024) void experts_scan_kernel(int32_t* __restrict__ blockcounts, int nblk, int64_t n,
-                                                            int64_t pairs, int E, int slots, int rows,
-                                                            int32_t* __restrict__ offsets, int32_t* __restrict__ tiles,
-                                                            int32_t* __restrict__ n_tiles) {
-  __shared__ int32_t total[kMaxExpertSlots + 1], first[kMaxExpertSlots + 1], tile0[kMaxExpertSlots + 1];
-  for (int e = threadIdx.x; e < slots; e += 1024) {
-    if (e < E) {
-      int32_t run = 0;
-      for (int b = 0; b < nblk; ++b) {
-        const int32_t c = blockcounts[(int64_t)b * E + e];
-        blockcounts[(int64_t)b * E + e] = run;
-        run += c;
+// order[next[e]++] = pair, next[] in LDS.  Places inside a slot are taken in whatever
+// order: a pair's results do not depend on its place.
+__device__ __forceinline__ void place_pairs(const int32_t* __restrict__ topk, int64_t from, int64_t to, int E,
+                                            int32_t* next, int32_t* __restrict__ order) {
+  for (int64_t i = from + threadIdx.x; i < to; i += kPlanThreads) {
+    const int e = topk[i];
+    if (e >= 0 && e < E) order[atomicAdd(&next[e], 1)] = (int32_t)i;
+  }
+}
+
+// Quantizes x (all of it, from the workgroups after the first) and, in workgroup 0,
+// makes the whole plan of at most kPlanPairs pairs.
+__global__ __launch_bounds__(kPlanThreads) void experts_begin_kernel(ExpertsPlan p, const uint16_t* __restrict__ x) {
+  __shared__ int32_t cnt[kMaxExperts], first[kMaxExperts], wave_sum[kPlanThreads / 64];
+  if (blockIdx.x > 0) {
+    const int64_t i = (int64_t)(blockIdx.x - 1) * kPlanThreads + threadIdx.x;
+    if (i < (int64_t)p.n * (p.d / 8)) mx_quantize8(x + 8 * i, i, p.xq, p.xs);
+    return;
+  }
+  count_pairs(p.topk, 0, p.pairs, p.E, cnt);
+  plan_tiles(cnt, first, wave_sum, p.E, p.E + p.shared, p.n, p.pairs, p.tile_rows, p.tiles, p.n_tiles);
+  place_pairs(p.topk, 0, p.pairs, p.E, first, p.order);
+}
+
+__global__ __launch_bounds__(kPlanThreads) void experts_count_kernel(ExpertsPlan p) {
+  __shared__ int32_t cnt[kMaxExperts];
+  const int64_t from = (int64_t)blockIdx.x * kPlanPairs;
+  count_pairs(p.topk, from, min(from + kPlanPairs, (int64_t)p.pairs), p.E, cnt);
+  for (int e = threadIdx.x; e < p.E; e += kPlanThreads) p.blockcounts[(int64_t)blockIdx.x * p.E + e] = cnt[e];
+}
+
+// One workgroup: each block's base within its slot (two threads per slot, each over
+// half of the blocks, eight counts loaded together), then offsets and tiles.
+__global__ __launch_bounds__(kPlanThreads) void experts_scan_kernel(ExpertsPlan p, int nblk) {
+  __shared__ int32_t cnt[kMaxExperts], first[kMaxExperts], wave_sum[kPlanThreads / 64];
+  const int e = threadIdx.x >> 1, part = threadIdx.x & 1;
+  const int lo = part * (nblk / 2), hi = part ? nblk : nblk / 2;
+  auto over = [&](int32_t run, bool write) {
+    for (int b = lo; b < hi; b += 8) {
+      int32_t c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = b + j < hi ? p.blockcounts[(int64_t)(b + j) * p.E + e] : 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (write && b + j < hi) p.blockcounts[(int64_t)(b + j) * p.E + e] = run;
+        run += c[j];
       }
-      total[e] = run;
-    } else {
-      total[e] = (int32_t)n;
     }
+    return run;
+  };
+  const int32_t sum = e < p.E ? over(0, false) : 0;
+  const int32_t before = __shfl(sum, (threadIdx.x & 63) & ~1);   // of the first half
+  if (e < p.E) {
+    over(part ? before : 0, true);
+    if (part) cnt[e] = before + sum;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int32_t o = 0, t = 0;
-    for (int e = 0; e < slots; ++e) {
-      first[e] = e < E ? o : (int32_t)(pairs + (int64_t)(e - E) * n);
-      if (e < E) o += total[e];
-      tile0[e] = t;
-      t += (total[e] + rows - 1) / rows;
-    }
-    *n_tiles = t;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < slots; e += 1024) {
-    if (e < E) offsets[e] = first[e];
-    for (int i = 0; i * rows < total[e]; ++i) {
-      int32_t* d = tiles + 3 * (int64_t)(tile0[e] + i);
-      d[0] = e;
-      d[1] = first[e] + i * rows;
-      d[2] = min(rows, total[e] - i * rows);
-    }
-  }
+  plan_tiles(cnt, first, wave_sum, p.E, p.E + p.shared, p.n, p.pairs, p.tile_rows, p.tiles, p.n_tiles);
+  for (int i = threadIdx.x; i < p.E; i += kPlanThreads) p.offsets[i] = first[i];
 }
 
-// order[offset + rank] = pair.  Ranks inside a block come from LDS counters in
-// whatever order: a pair's results do not depend on its place in a tile.
-__global__ __launch_bounds__(256) void experts_scatter_kernel(const int32_t* __restrict__ topk, int64_t pairs, int E,
-                                                              const int32_t* __restrict__ blockbase,
-                                                              const int32_t* __restrict__ offsets,
-                                                              int32_t* __restrict__ order) {
+__global__ __launch_bounds__(kPlanThreads) void experts_scatter_kernel(ExpertsPlan p) {
   __shared__ int32_t next[kMaxExperts];
-  for (int e = threadIdx.x; e < E; e += 256) next[e] = offsets[e] + blockbase[(int64_t)blockIdx.x * E + e];
+  for (int e = threadIdx.x; e < p.E; e += kPlanThreads)
+    next[e] = p.offsets[e] + p.blockcounts[(int64_t)blockIdx.x * p.E + e];
   __syncthreads();
-  const int64_t base = (int64_t)blockIdx.x * kPlanPairs;
-  for (int i = threadIdx.x; i < kPlanPairs; i += 256) {
-    if (base + i >= pairs) break;
-    const int e = topk[base + i];
-    if (e >= 0 && e < E) order[atomicAdd(&next[e], 1)] = (int32_t)(base + i);
-  }
+  const int64_t from = (int64_t)blockIdx.x * kPlanPairs;
+  place_pairs(p.topk, from, min(from + kPlanPairs, (int64_t)p.pairs), p.E, next, p.order);
 }
 
 // ------------------------------------------------------------------ products
@@ -107,7 +161,53 @@ __device__ __forceinline__ int32_t token_of(const ExpertsPlan& p, int32_t pair) 
   return pair < p.pairs ? pair / p.K : (int32_t)((pair - p.pairs) % p.n);
 }
 
+__device__ __forceinline__ void store_y(void* out, bool bf16, int64_t at, f32x4 y) {
+  if (bf16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+        make_uint2(mx_bf16_pair(y[0], y[1]), mx_bf16_pair(y[2], y[3]));
+  else
+    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = y;
+}
+
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// The sums of fragment m over the waves, SwiGLU and quantization of feature block
+// `block` of positions pos0 + 0 .. min(rows, 16) - 1: a position's 32 features are in the
+// four lanes r + 16 q, eight each (4 q + 0..3 of both halves).
+template <int WAVES, int MF>
+__device__ __forceinline__ void experts_h(const ExpertsPlan& p, const f32x4 (&part)[WAVES][4 * MF][64], int m, int pos0,
+                                          int rows, int block) {
+  const int lane = threadIdx.x & 63, r = lane & 15;
+  float v[8];
+  f32x4 s[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    s[a] = part[0][a * MF + m][lane];
+#pragma unroll
+    for (int u = 1; u < WAVES; ++u) s[a] += part[u][a * MF + m][lane];
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = swiglu(s[i >> 2][i & 3], s[2 + (i >> 2)][i & 3]);
+    const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
+    top = u > top ? u : top;
+  }
+#pragma unroll
+  for (int o = 16; o < 64; o <<= 1) {
+    const uint32_t u = __shfl_xor(top, o);
+    top = u > top ? u : top;
+  }
+  const int sb = mx_scale_byte(top);
+  const uint32_t q = sb == kMxNan ? 0u : mx_codes8(v, sb);   // low half: features 4q.., high half: 16 + 4q..
+  if (r < rows) {
+    const int64_t at = (int64_t)(pos0 + r) * (p.f / kMxBlock) + block;
+    uint16_t* dst = reinterpret_cast<uint16_t*>(p.hq + at * kMxBlockBytes);
+    dst[lane >> 4] = (uint16_t)q;
+    dst[4 + (lane >> 4)] = (uint16_t)(q >> 16);
+    if (lane < 16) p.hs[at] = (uint8_t)sb;
+  }
+}
 
 // First product, SwiGLU and quantization: a workgroup owns 32 features (their
 // gate and up rows: four fragments of 16) of one tile of up to 16 MF positions.
@@ -142,39 +242,7 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_stream_kernel(ExpertsPl
 #pragma unroll
     for (int m = 0; m < MF; ++m) part[wave][a * MF + m][lane] = acc[a][m];
   __syncthreads();
-  // position r of fragment m: its 32 features are in the four lanes r + 16 q,
-  // eight each (4 q + 0..3 of both halves)
-  for (int m = wave; m < MF; m += WAVES) {
-    float v[8];
-    f32x4 s[4];
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      s[a] = part[0][a * MF + m][lane];
-#pragma unroll
-      for (int u = 1; u < WAVES; ++u) s[a] += part[u][a * MF + m][lane];
-    }
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = swiglu(s[i >> 2][i & 3], s[2 + (i >> 2)][i & 3]);
-      const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
-      top = u > top ? u : top;
-    }
-#pragma unroll
-    for (int o = 16; o < 64; o <<= 1) {
-      const uint32_t u = __shfl_xor(top, o);
-      top = u > top ? u : top;
-    }
-    const int sb = mx_scale_byte(top);
-    const uint32_t q = sb == kMxNan ? 0u : mx_codes8(v, sb);   // low half: features 4q.., high half: 16 + 4q..
-    if (16 * m + r < rows) {
-      const int64_t at = (int64_t)(pos0 + 16 * m + r) * (p.f / kMxBlock) + blockIdx.y;
-      uint16_t* dst = reinterpret_cast<uint16_t*>(p.hq + at * kMxBlockBytes);
-      dst[lane >> 4] = (uint16_t)q;
-      dst[4 + (lane >> 4)] = (uint16_t)(q >> 16);
-      if (lane < 16) p.hs[at] = (uint8_t)sb;
-    }
-  }
+  for (int m = wave; m < MF; m += WAVES) experts_h<WAVES, MF>(p, part, m, pos0 + 16 * m, rows - 16 * m, blockIdx.y);
 }
 
 // Second product: 16 model features of one tile.
@@ -211,6 +279,77 @@ __global__ __launch_bounds__(64 * WAVES) void experts_down_stream_kernel(Experts
       *reinterpret_cast<f32x4*>(p.ypair + pair * p.d + c0 + 4 * (lane >> 4)) = v;
     }
   }
+}
+
+// ------------------------------------------------------------------ a few tokens
+// Without a plan: a workgroup per (pair, 32 features), then per (token, 16 model
+// features).  Every pair reads its expert's weights itself; h goes by pair.
+
+__device__ __forceinline__ int slot_of(const ExpertsPlan& p, int32_t pair) {
+  return pair < p.pairs ? p.topk[pair] : p.E + (pair - p.pairs) / p.n;
+}
+
+// First product: the token's row is quantized into LDS by each of its workgroups (4 KB
+// of x against 64 rows of weights), the waves split the contraction.
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void experts_up_few_kernel(ExpertsPlan p, const uint16_t* __restrict__ x) {
+  __shared__ f32x4 part[WAVES][4][64];
+  __shared__ __attribute__((aligned(16))) uint8_t xq[kMaxD / 2], xs[kMaxD / kMxBlock];
+  const int32_t pair = blockIdx.x;
+  const int e = slot_of(p, pair);
+  if (pair < p.pairs && (e < 0 || e >= p.E)) return;
+  const uint16_t* row = x + (int64_t)token_of(p, pair) * p.d;
+  for (int i = threadIdx.x; i < p.d / 8; i += 64 * WAVES) mx_quantize8(row + 8 * i, i, xq, xs);
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
+  const int f0 = blockIdx.y * 32, nb = p.d / kMxBlock;
+  MxRow wrow[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {   // gate features 0-15, 16-31, then up
+    const int64_t at = (int64_t)e * 2 * p.f + (a >> 1) * p.f + f0 + 16 * (a & 1) + r;
+    wrow[a] = {p.wgu + at * nb * kMxBlockBytes, p.wgu_scales + at * nb};
+  }
+  const MxRow xrow[1] = {{xq, xs}};   // the same row in all 16 columns
+  f32x4 acc[4][1];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) acc[a][0] = f32x4{0, 0, 0, 0};
+  mx_stream<4, 1>(wrow, xrow, nb, wave, WAVES, acc);
+#pragma unroll
+  for (int a = 0; a < 4; ++a) part[wave][a][lane] = acc[a][0];
+  __syncthreads();
+  if (wave > 0) return;
+  experts_h<WAVES, 1>(p, part, 0, pair, 1, blockIdx.y);
+}
+
+// Second product and the sum over the token's pairs, in order: a wave per pair, as
+// many rounds of WAVES pairs as it takes.
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void experts_down_few_kernel(ExpertsPlan p, void* __restrict__ out, bool bf16) {
+  __shared__ f32x4 part[WAVES][4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int t = blockIdx.x, c0 = blockIdx.y * 16, nb = p.f / kMxBlock;
+  f32x4 y = {0, 0, 0, 0};
+  for (int j0 = 0; j0 < p.K + p.shared; j0 += WAVES) {
+    const int j = j0 + wave;
+    f32x4 acc[1][1] = {{f32x4{0, 0, 0, 0}}};
+    if (j < p.K + p.shared) {
+      const int32_t pair = j < p.K ? t * p.K + j : p.pairs + (j - p.K) * p.n + t;
+      const int e = slot_of(p, pair);
+      if (j >= p.K || (e >= 0 && e < p.E)) {
+        const int64_t wr = (int64_t)e * p.d + c0 + r;
+        const MxRow w[1] = {{p.wd + wr * nb * kMxBlockBytes, p.wd_scales + wr * nb}};
+        const MxRow h[1] = {{p.hq + (int64_t)pair * nb * kMxBlockBytes, p.hs + (int64_t)pair * nb}};
+        mx_stream<1, 1>(w, h, nb, 0, 1, acc);
+        acc[0][0] *= j < p.K ? p.weights[pair] : 1.0f;
+      }
+    }
+    if (r == 0) part[wave][g] = acc[0][0];
+    __syncthreads();
+    if (wave == 0 && lane < 4)
+      for (int w = 0; w < WAVES && j0 + w < p.K + p.shared; ++w) y += part[w][lane];
+    __syncthreads();
+  }
+  if (wave == 0 && lane < 4) store_y(out, bf16, (int64_t)t * p.d + c0 + 4 * lane, y);
 }
 
 // ------------------------------------------------------------------ products over many positions
@@ -335,14 +474,7 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(ExpertsPlan p, voi
   }
   for (int s = 0; s < p.shared; ++s)
     y += *reinterpret_cast<const f32x4*>(p.ypair + (p.pairs + (int64_t)s * p.n + t) * p.d + c);
-  if (bf16) {
-    uint2 q;
-    q.x = mx_bf16(y[0]) | ((uint32_t)mx_bf16(y[1]) << 16);
-    q.y = mx_bf16(y[2]) | ((uint32_t)mx_bf16(y[3]) << 16);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + t * p.d + c) = q;
-  } else {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + t * p.d + c) = y;
-  }
+  store_y(out, bf16, t * p.d + c, y);
 }
 
 // Positions of a tile of the plan, from the mean number of a routed slot's positions
@@ -356,6 +488,9 @@ int experts_tile_rows(int64_t n, int d, int f, int K, int E) {
   return mean >= 48 ? 128 : mean >= 8 ? 64 : 16;
 }
 int experts_plan_blocks(int64_t pairs) { return (int)((pairs + kPlanPairs - 1) / kPlanPairs); }
+
+// Pairs up to which every pair reads its expert's weights itself.
+constexpr int64_t kFewPairs = 32;
 
 namespace {
 template <class T, bool UP, bool DOWN>   // whether the rows' scales of each product are whole words
@@ -374,13 +509,22 @@ void run_stream(const ExpertsPlan& p, hipStream_t s) {
 }  // namespace
 
 void launch_experts(const ExpertsPlan& p, const uint16_t* x, void* out, bool bf16, hipStream_t s) {
-  launch_mx_quantize(x, true, p.n, p.d, p.d, p.xq, p.xs, s);
-  const int nblk = experts_plan_blocks(p.pairs);
-  hipLaunchKernelGGL(experts_count_kernel, dim3(nblk), dim3(256), 0, s, p.topk, p.pairs, p.E, p.blockcounts);
-  hipLaunchKernelGGL(experts_scan_kernel, dim3(1), dim3(1024), 0, s, p.blockcounts, nblk, p.n, p.pairs, p.E,
-                     p.E + p.shared, p.tile_rows, p.offsets, p.tiles, p.n_tiles);
-  hipLaunchKernelGGL(experts_scatter_kernel, dim3(nblk), dim3(256), 0, s, p.topk, p.pairs, p.E, p.blockcounts,
-                     p.offsets, p.order);
+  const int64_t all = (int64_t)p.n * (p.K + p.shared), chunks = (int64_t)p.n * (p.d / 8);
+  if (all <= kFewPairs) {
+    hipLaunchKernelGGL(experts_up_few_kernel<8>, dim3((unsigned)all, p.f / 32), dim3(512), 0, s, p, x);
+    hipLaunchKernelGGL(experts_down_few_kernel<8>, dim3(p.n, p.d / 16), dim3(512), 0, s, p, out, bf16);
+    return;
+  }
+  if (p.pairs <= kPlanPairs) {
+    hipLaunchKernelGGL(experts_begin_kernel, dim3((unsigned)(1 + (chunks + kPlanThreads - 1) / kPlanThreads)),
+                       dim3(kPlanThreads), 0, s, p, x);
+  } else {
+    const int nblk = experts_plan_blocks(p.pairs);
+    launch_mx_quantize(x, true, p.n, p.d, p.d, p.xq, p.xs, s);
+    hipLaunchKernelGGL(experts_count_kernel, dim3(nblk), dim3(kPlanThreads), 0, s, p);
+    hipLaunchKernelGGL(experts_scan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p, nblk);
+    hipLaunchKernelGGL(experts_scatter_kernel, dim3(nblk), dim3(kPlanThreads), 0, s, p);
+  }
   switch (p.tile_rows) {
     case 256: run_tiles<Tile256, true, true>(p, s); break;
     case 128: {

@@ -13,6 +13,7 @@ namespace clha {
 constexpr int kBucketTokens = 1024;   // tokens per bucketing workgroup (16 groups of 64)
 constexpr int kTokPad = 64;           // expert token lists are padded to this multiple
 constexpr int kMaxExperts = 256;
+constexpr int kMaxD = 8192;           // hidden size
 constexpr int kMaxTopK = 16;
 constexpr int kMaxLayers = 8;
 constexpr int kSyrkTile = 256;        // Gram-sum output tile

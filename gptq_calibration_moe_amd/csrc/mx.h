@@ -75,4 +75,31 @@ __device__ __forceinline__ uint32_t mx_codes8(const float* v, int scale_byte) {
   return q;
 }
 
+// Eight bf16 values at v (chunk i of a run of whole blocks): codes and scales, four
+// neighbouring lanes per block.
+__device__ __forceinline__ void mx_quantize8(const uint16_t* v, int64_t i, uint8_t* codes, uint8_t* scales) {
+  const uint4 q = *reinterpret_cast<const uint4*>(v);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  float f[8];
+  uint32_t m = 0;   // magnitudes compare as their bits; NaN and infinity are the largest
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = __uint_as_float(w[j] << 16);
+    f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t u = __float_as_uint(f[j]) & 0x7fffffffu;
+    m = u > m ? u : m;
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const uint32_t u = __shfl_xor(m, o);
+    m = u > m ? u : m;
+  }
+  const int sb = mx_scale_byte(m);
+  reinterpret_cast<uint32_t*>(codes)[i] = sb == kMxNan ? 0u : mx_codes8(f, sb);
+  if ((i & 3) == 0) scales[i >> 2] = (uint8_t)sb;
+}
+
 }  // namespace clha
