@@ -298,9 +298,6 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_few_kernel(ExpertsPlan 
   const int32_t pair = blockIdx.x;
   const int e = slot_of(p, pair);
   if (pair < p.pairs && (e < 0 || e >= p.E)) return;
-  const uint16_t* row = x + (int64_t)token_of(p, pair) * p.d;
-  for (int i = threadIdx.x; i < p.d / 8; i += 64 * WAVES) mx_quantize8(row + 8 * i, i, xq, xs);
-  __syncthreads();
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
   const int f0 = blockIdx.y * 32, nb = p.d / kMxBlock;
   MxRow wrow[4];
@@ -309,11 +306,19 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_few_kernel(ExpertsPlan 
     const int64_t at = (int64_t)e * 2 * p.f + (a >> 1) * p.f + f0 + 16 * (a & 1) + r;
     wrow[a] = {p.wgu + at * nb * kMxBlockBytes, p.wgu_scales + at * nb};
   }
+  // the wave's first chunk of weights is on its way while x is quantized
+  MxPair pw[4], px[1];
+  mx_load_chunk(wrow, wave, nb, pw);
+  const uint16_t* row = x + (int64_t)token_of(p, pair) * p.d;
+  for (int i = threadIdx.x; i < p.d / 8; i += 64 * WAVES) mx_quantize8(row + 8 * i, i, xq, xs);
+  __syncthreads();
   const MxRow xrow[1] = {{xq, xs}};   // the same row in all 16 columns
   f32x4 acc[4][1];
 #pragma unroll
   for (int a = 0; a < 4; ++a) acc[a][0] = f32x4{0, 0, 0, 0};
-  mx_stream<4, 1>(wrow, xrow, nb, wave, WAVES, acc);
+  mx_load_chunk(xrow, wave, nb, px);
+  mx_multiply(pw, px, acc);   // (a chunk past the end is zeros)
+  mx_stream<4, 1>(wrow, xrow, nb, wave + WAVES, WAVES, acc);
 #pragma unroll
   for (int a = 0; a < 4; ++a) part[wave][a][lane] = acc[a][0];
   __syncthreads();

@@ -42,27 +42,37 @@ __device__ __forceinline__ MxPair mx_load_pair(const MxRow& r, int b, int nb) {
   return p;
 }
 
-// acc[a][m] += W rows (NA fragments of 16) times x rows (MF fragments of 16)
-// over the chunks c0, c0 + step, ... of nb blocks.
+template <int N>
+__device__ __forceinline__ void mx_load_chunk(const MxRow (&row)[N], int c, int nb, MxPair (&to)[N]) {
+  const int b = 8 * c + 2 * ((threadIdx.x & 63) >> 4);
+#pragma unroll
+  for (int i = 0; i < N; ++i) to[i] = mx_load_pair(row[i], b, nb);
+}
+
+// acc[a][m] += W rows (NA fragments of 16) times x rows (MF fragments of 16) of one chunk.
+template <int NA, int MF>
+__device__ __forceinline__ void mx_multiply(const MxPair (&pw)[NA], const MxPair (&px)[MF], f32x4 (&acc)[NA][MF]) {
+#pragma unroll
+  for (int a = 0; a < NA; ++a)
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      acc[a][m] = mx_mfma16<0>(pw[a].q0, px[m].q0, acc[a][m], pw[a].s, px[m].s);
+      acc[a][m] = mx_mfma16<1>(pw[a].q1, px[m].q1, acc[a][m], pw[a].s, px[m].s);
+    }
+}
+
+// The chunks c0, c0 + step, ... of nb blocks.  One at a time: holding the next one's
+// operands too costs more waves per CU than it hides (48 tokens through 66 experts'
+// first product: 47 us against 40).
 template <int NA, int MF>
 __device__ __forceinline__ void mx_stream(const MxRow (&w)[NA], const MxRow (&x)[MF], int nb, int c0, int step,
                                           f32x4 (&acc)[NA][MF]) {
-  const int g = (threadIdx.x & 63) >> 4;
   const int chunks = (nb + 7) / 8;
   for (int c = c0; c < chunks; c += step) {
-    const int b = 8 * c + 2 * g;
     MxPair pw[NA], px[MF];
-#pragma unroll
-    for (int a = 0; a < NA; ++a) pw[a] = mx_load_pair(w[a], b, nb);
-#pragma unroll
-    for (int m = 0; m < MF; ++m) px[m] = mx_load_pair(x[m], b, nb);
-#pragma unroll
-    for (int a = 0; a < NA; ++a)
-#pragma unroll
-      for (int m = 0; m < MF; ++m) {
-        acc[a][m] = mx_mfma16<0>(pw[a].q0, px[m].q0, acc[a][m], pw[a].s, px[m].s);
-        acc[a][m] = mx_mfma16<1>(pw[a].q1, px[m].q1, acc[a][m], pw[a].s, px[m].s);
-      }
+    mx_load_chunk(w, c, nb, pw);
+    mx_load_chunk(x, c, nb, px);
+    mx_multiply(pw, px, acc);
   }
 }
 

@@ -8,16 +8,24 @@
 // lower index; weights are the chosen scores, optionally over their sum, times a
 // factor.
 //
-// The order of two close choices decides whole numbers, so c and the marks are
-// formed in 64 bits whenever they are more than a logit.
+// The order of two close choices decides whole numbers, so it is that of 64-bit
+// choices and marks wherever they are more than a logit.  Forming those for every
+// expert took most of the time (32749 tokens, 256 experts in 8 groups, sigmoid with a
+// bias: 93 us).  Instead the candidates are found in 32 bits with a bound on the error:
+// the list runs on behind the K-th choice to the first gap that the bound cannot
+// close, so it holds the K best.  Where its order is not certain either, each lane
+// forms the 64-bit choice of its candidate and counts those ahead of it; close groups
+// are told apart by the 64-bit choices of the one or two experts that make each mark.
+// Only a token that this leaves open (more than 16 close choices, close groups with close
+// members, more than 16 groups) is done wholly in 64 bits: 25 us for one wave of those.
 //
 // Layout: 16 lanes per token, lane i holds experts i*V .. i*V+V-1 (V = E/16
 // rounded up to a power of two), so a token's logits are read as one contiguous
 // run and lower lanes hold lower indices.  Values become unsigned keys of the
-// same order, with 0 for an expert that is taken, masked or beyond E; every
-// round takes the largest key (four lane exchanges), the lowest lane holding it
-// and that lane's lowest place.  Keys of real experts are never 0, so the ids of
-// a token are distinct and in range even for logits that are not finite.
+// same order, with 0 for an expert that is taken, masked or beyond E; a round takes the
+// largest key, whose low bits name its place in the lane.  Keys of real experts are
+// never 0, so the ids of a token are distinct and in range even for logits that are not
+// finite.
 #include "kernels.h"
 
 namespace clha {
@@ -25,11 +33,34 @@ namespace clha {
 constexpr int kRL = 16;              // lanes per token (>= kMaxTopK)
 constexpr int kRTokens = 256 / kRL;  // tokens per workgroup
 
-template <typename T>
-__device__ __forceinline__ T lane_max(T v) {
+// Of the 16 lanes of a token: one data-parallel row of the wave.
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_move(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+constexpr int kSwap1 = 0xb1, kSwap2 = 0x4e, kMirror8 = 0x141, kMirror16 = 0x140;
+__device__ __forceinline__ uint32_t lane_max(uint32_t v) {
+  v = max(v, row_move<kSwap1>(v));
+  v = max(v, row_move<kSwap2>(v));
+  v = max(v, row_move<kMirror8>(v));
+  return max(v, row_move<kMirror16>(v));
+}
+__device__ __forceinline__ float lane_max(float v) {
+  v = fmaxf(v, __uint_as_float(row_move<kSwap1>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(row_move<kSwap2>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(row_move<kMirror8>(__float_as_uint(v))));
+  return fmaxf(v, __uint_as_float(row_move<kMirror16>(__float_as_uint(v))));
+}
+__device__ __forceinline__ float lane_sum(float v) {
+  v += __uint_as_float(row_move<kSwap1>(__float_as_uint(v)));
+  v += __uint_as_float(row_move<kSwap2>(__float_as_uint(v)));
+  v += __uint_as_float(row_move<kMirror8>(__float_as_uint(v)));
+  return v + __uint_as_float(row_move<kMirror16>(__float_as_uint(v)));
+}
+__device__ __forceinline__ unsigned long long lane_max(unsigned long long v) {
 #pragma unroll
   for (int o = 1; o < kRL; o <<= 1) {
-    const T w = __shfl_xor(v, o, kRL);
+    const unsigned long long w = __shfl_xor(v, o, kRL);
     v = w > v ? w : v;
   }
   return v;
@@ -39,6 +70,12 @@ __device__ __forceinline__ double lane_sum(double v) {
   for (int o = 1; o < kRL; o <<= 1) v += __shfl_xor(v, o, kRL);
   return v;
 }
+// The bits of a wave's vote that belong to this token's lanes.
+__device__ __forceinline__ uint32_t row_vote(bool b) {
+  return (uint32_t)(__ballot(b) >> ((threadIdx.x & 63) / kRL * kRL)) & 0xffffu;
+}
+// A token's LDS is written and read by lanes of one wave, whose accesses stay in order.
+__device__ __forceinline__ void wave_sync() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // Order-preserving unsigned keys (x + 0 makes the two zeros equal); never 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -46,152 +83,401 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t k = u >> 31 ? ~u : u | 0x80000000u;
   return k ? k : 1u;
 }
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k); }
 __device__ __forceinline__ unsigned long long order_key(double x) {
   const unsigned long long u = __double_as_longlong(x + 0.0);
   const unsigned long long k = u >> 63 ? ~u : u | (1ull << 63);
   return k ? k : 1ull;
 }
 
-template <bool WIDE>
-struct KeyOf {
-  typedef uint32_t type;
-};
-template <>
-struct KeyOf<true> {
-  typedef unsigned long long type;
+// What of a routing the two passes share.
+struct RouteRow {
+  int E, K, lane;
+  float top;     // largest logit
+  RouteArgs a;
 };
 
-// WIDE: the choice is s + b in 64 bits (a bias is given); otherwise the logit.
-// GROUPS: more than one group.
-template <int V, bool WIDE, bool GROUPS>
-__global__ __launch_bounds__(256) void score_route_kernel(const float* __restrict__ logits,
-                                                          const float* __restrict__ bias, int64_t n, int E, int K,
-                                                          RouteArgs a, int32_t* __restrict__ topk,
-                                                          float* __restrict__ weights, int32_t* __restrict__ iota,
-                                                          int* __restrict__ status, int layer, int has_layer) {
-  typedef typename KeyOf<WIDE>::type Key;
-  __shared__ double member[GROUPS ? kRTokens * kMaxExperts : 1];
-  __shared__ double mark[GROUPS ? kRTokens * kMaxExperts : 1];
-  __shared__ uint32_t keep[GROUPS ? kRTokens * (kMaxExperts / 32) : 1];
-  const int lane = threadIdx.x % kRL, slot = threadIdx.x / kRL;
-  const int64_t t = (int64_t)blockIdx.x * kRTokens + slot;
-  const float* row = logits + (t < n ? t : n - 1) * E;   // tokens past the end repeat the last one
-  float l[V];
-  bool bad = false;
-  float top = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane * V + j;
-    l[j] = e < E ? row[e] : 0.0f;
-    if (e < E) {
-      bad |= !isfinite(l[j]);
-      top = fmaxf(top, l[j]);
-    }
-  }
-  top = lane_max(top);
-  const bool soft = a.score == kScoreSoftmax;
-  double s[V];          // scores in 64 bits, where the choice or the marks need them
-  double den = 1.0;     // sum of exp(l - top)
-  const bool marks_by_score = GROUPS && a.group_score == kGroupTop2;
-  if (WIDE || marks_by_score) {
-    double sum = 0.0;
+// The marks of the groups g = lane + 16 j, then the marks in LDS from mem on.  Where
+// no lane's experts are of two groups, lanes reduce their own values first.
+template <int V>
+__device__ __forceinline__ void group_marks(const RouteRow& q, const float (&v)[V], float* mem, float (&mk)[V]) {
+  const int per = q.E / q.a.n_groups;
+  const bool whole = per % V == 0;
+  float own1 = -INFINITY, own2 = -INFINITY;
+  if (whole) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int e = lane * V + j;
-      s[j] = soft ? exp((double)l[j] - (double)top) : 1.0 / (1.0 + exp(-(double)l[j]));
-      if (e < E) sum += s[j];
+      const float x = q.lane * V + j < q.E ? v[j] : -INFINITY;
+      own2 = fmaxf(own2, fminf(own1, x));
+      own1 = fmaxf(own1, x);
     }
-    if (soft) {
-      den = lane_sum(sum);
-#pragma unroll
-      for (int j = 0; j < V; ++j) s[j] /= den;
-    }
-  } else if (soft && !a.renormalize) {
-    double sum = 0.0;
+    mem[2 * q.lane] = own1;
+    mem[2 * q.lane + 1] = own2;
+  } else {
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (lane * V + j < E) sum += (double)expf(l[j] - top);
-    den = lane_sum(sum);
+      if (q.lane * V + j < q.E) mem[q.lane * V + j] = v[j];
   }
-  Key key[V];
+  wave_sync();
+  const int parts = whole ? per / V : per, words = whole ? 2 : 1;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int e = lane * V + j;
-    if constexpr (WIDE) {
-      const float b = e < E ? bias[e] : 0.0f;
-      bad |= !isfinite(b);
-      s[j] += (double)b;
-      key[j] = e < E ? order_key(s[j]) : 0;
-    } else {
-      key[j] = e < E ? order_key(l[j]) : 0;
+    const int g = q.lane + kRL * j;
+    float m1 = -INFINITY, m2 = -INFINITY;
+    if (g < q.a.n_groups) {
+      const float* from = mem + g * parts * words;
+      for (int i = 0; i < parts * words; ++i) {
+        const float x = from[i];
+        m2 = fmaxf(m2, fminf(m1, x));
+        m1 = fmaxf(m1, x);
+      }
     }
+    mk[j] = q.a.group_score == kGroupTop2 && per > 1 ? m1 + m2 : m1;
+    if (kRL * (j + 1) >= q.a.n_groups) break;
   }
-  if constexpr (GROUPS) {
-    const int per = E / a.n_groups;
-    double* mem = member + slot * kMaxExperts;
-    double* mk = mark + slot * kMaxExperts;
-    uint32_t* kp = keep + slot * (kMaxExperts / 32);
+  wave_sync();
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (lane * V + j < E) mem[lane * V + j] = WIDE || marks_by_score ? s[j] : (double)l[j];
-    if (lane < kMaxExperts / 32) kp[lane] = 0;
-    __syncthreads();
-    for (int g = lane; g < a.n_groups; g += kRL) {
+  for (int j = 0; j < V; ++j)
+    if (q.lane + kRL * j < q.a.n_groups) mem[q.lane + kRL * j] = mk[j];
+  wave_sync();
+}
+
+// The exact score of logit l, before a softmax's division by its sum of exp(l - top).
+// (One exponential in the code: this path is seldom run, and fetching its instructions
+// for the first time takes longer than running them.)
+__device__ __forceinline__ double exact_score(bool soft, float l, float top) {
+  const double x = exp(soft ? (double)l - (double)top : -(double)l);
+  return soft ? x : 1.0 / (1.0 + x);
+}
+
+// The whole choice in 64 bits (logits where it is no more than one).  Loops over LDS and
+// the logits in memory: it is rare, and its registers would cost the usual path its
+// occupancy.  Returns round `lane`'s expert.
+template <int V>
+__device__ __forceinline__ int route_exact(const float* row, const float* __restrict__ bias, const RouteRow& q,
+                                           double* mem, double* marks) {
+  const int lane = q.lane, E = q.E, G = q.a.n_groups, per = E / G;
+  const int e0 = lane * V, e1 = min(e0 + V, E);
+  const bool top2 = q.a.group_score == kGroupTop2 && per > 1;
+  const bool by_score = bias || (G > 1 && q.a.group_score == kGroupTop2);
+  const bool soft = q.a.score == kScoreSoftmax;
+  double den = 0.0;
+  wave_sync();
+#pragma unroll 1
+  for (int e = e0; e < e1; ++e) {
+    const double v = by_score ? exact_score(soft, row[e], q.top) : (double)row[e];
+    mem[e] = v;
+    den += v;
+  }
+  den = lane_sum(den);
+  if (by_score)
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) mem[e] = (soft ? mem[e] / den : mem[e]) + (bias ? (double)bias[e] : 0.0);
+  wave_sync();
+  uint32_t alive = 0;   // of this lane's experts
+  if (G > 1) {
+    auto mark = [&](int g) {
       double m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll 1
       for (int i = 0; i < per; ++i) {
         const double v = mem[g * per + i];
         m2 = fmax(m2, fmin(m1, v));
         m1 = fmax(m1, v);
       }
-      mk[g] = a.group_score == kGroupTop2 && per > 1 ? m1 + m2 : m1;
-    }
-    __syncthreads();
-    for (int g = lane; g < a.n_groups; g += kRL) {
-      const unsigned long long mine = order_key(mk[g]);
+      return top2 ? m1 + m2 : m1;
+    };
+    const bool kept = G <= kRL;   // a mark per lane; more groups' marks are formed again where they are compared
+    if (kept && lane < G) marks[lane] = mark(lane);
+    wave_sync();
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+      const int g = e / per;
+      if (e > e0 && g == (e - 1) / per) {   // as the expert before
+        alive |= (alive >> (e - 1 - e0) & 1u) << (e - e0);
+        continue;
+      }
+      const unsigned long long mine = order_key(kept ? marks[g] : mark(g));
       int better = 0;
-      for (int o = 0; o < a.n_groups; ++o) {
-        const unsigned long long other = order_key(mk[o]);
+#pragma unroll 1
+      for (int o = 0; o < G; ++o) {
+        const unsigned long long other = order_key(kept ? marks[o] : mark(o));
         better += other > mine || (other == mine && o < g);
       }
-      if (better < a.top_groups) atomicOr(&kp[g >> 5], 1u << (g & 31));
+      alive |= (uint32_t)(better < q.a.top_groups) << (e - e0);
     }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int g = (lane * V + j) / per;
-      if (lane * V + j < E && !((kp[g >> 5] >> (g & 31)) & 1u)) key[j] = 0;
-    }
+  } else {
+    alive = e1 > e0 ? (1u << (e1 - e0)) - 1u : 0u;
   }
-  int chosen = 0;   // of round `lane`
-  for (int k = 0; k < K; ++k) {
-    Key best = 0;
+  int chosen = 0;
+#pragma unroll 1
+  for (int k = 0; k < q.K; ++k) {
+    unsigned long long best = 0;
     int at = 0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (key[j] > best) {
-        best = key[j];
-        at = j;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+      const unsigned long long key = bias ? order_key(mem[e]) : (unsigned long long)order_key(row[e]);
+      if ((alive >> (e - e0) & 1u) && key > best) {
+        best = key;
+        at = e;
       }
     }
-    const Key m = lane_max(best);
-    const unsigned long long vote = __ballot(best == m);
-    const int first = __ffs((unsigned)(vote >> ((threadIdx.x & 63) / kRL * kRL)) & 0xffffu) - 1;
-    const int e = __shfl(lane * V + at, first, kRL);
+    const unsigned long long m = lane_max(best);
+    const int first = __ffs(row_vote(best == m)) - 1;
+    const int e = __shfl(at, first, kRL);
     if (lane == k) chosen = e;
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (lane == first && j == at) key[j] = 0;
+    if (lane == first) alive &= ~(1u << (at - e0));
   }
+  return chosen;
+}
+
+// Marks too close for 32 bits (the lanes of a token come here together): lane g finds
+// the one or two experts that make group g's mark, forms their 64-bit choices and ranks
+// the exact marks; kp then holds the best groups.  False where an expert behind those
+// two is as close, or there are more groups than lanes.
+template <int V>
+__device__ __forceinline__ bool close_groups(const float (&s)[V], const float* row, const float* __restrict__ bias,
+                                             const RouteRow& q, float* mem, uint32_t* kp, double* marks) {
+  const int lane = q.lane, G = q.a.n_groups, per = q.E / G;
+  const bool soft = q.a.score == kScoreSoftmax, top2 = q.a.group_score == kGroupTop2 && per > 1;
+  if (G > kRL) return false;
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (lane * V + j < q.E) mem[lane * V + j] = s[j];
+  double den = 1.0;
+  if (soft) {
+    den = 0.0;
+#pragma unroll 1
+    for (int e = lane * V; e < min(lane * V + V, q.E); ++e) den += exact_score(true, row[e], q.top);
+    den = lane_sum(den);
+  }
+  if (lane < kMaxExperts / 32) kp[lane] = 0;
+  wave_sync();
+  bool sure = true;
+  if (lane < G) {
+    float m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+    int i1 = 0, i2 = 0;
+#pragma unroll 1
+    for (int e = lane * per; e < (lane + 1) * per; ++e) {
+      const float v = mem[e];
+      const bool a1 = v > m1, a2 = v > m2;
+      m3 = a2 ? m2 : fmaxf(m3, v);
+      i2 = a1 ? i1 : a2 ? e : i2;
+      m2 = a1 ? m1 : a2 ? v : m2;
+      i1 = a1 ? e : i1;
+      m1 = a1 ? v : m1;
+    }
+    const float last = top2 ? m2 : m1, next = top2 ? m3 : m2;
+    sure = last - next > 0x1p-18f * (1.0f + fabsf(last));
+    double mark = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < (top2 ? 2 : 1); ++i) {
+      const int e = i ? i2 : i1;
+      mark += exact_score(soft, row[e], q.top) / den + (bias ? (double)bias[e] : 0.0);
+    }
+    marks[lane] = mark;
+  }
+  wave_sync();
+  if (lane < G) {
+    const unsigned long long mine = order_key(marks[lane]);
+    int better = 0;
+#pragma unroll 1
+    for (int o = 0; o < G; ++o) {
+      const unsigned long long other = order_key(marks[o]);
+      better += other > mine || (other == mine && o < lane);
+    }
+    if (better < q.a.top_groups) atomicOr(&kp[0], 1u << lane);
+  }
+  wave_sync();
+  return row_vote(!sure) == 0;
+}
+
+// The usual path: round `lane`'s expert, or `hard` set where the token needs
+// route_exact.  Errors of the 32-bit values: a sigmoid is within 2^-22 (argument's
+// rounding, |l| 2^-24 weighted by s (1 - s), at most 0.23; a hardware exp2 and reciprocal, 1
+// unit in the last place each, and one addition); a softmax's exponentials are within
+// 2^-22 and their sum, one factor on all scores, within 2^-19 of itself.  Adding the
+// bias rounds by 2^-24 |c| and the key drops up to 4 bits, 2^-20 |c|.  So choices more than
+// 2^-18 (1 + |c|) apart, and marks (sums of two, no bits dropped) 2^-19 (1 + |mark|) apart,
+// 2^-17 for a softmax, are in their exact order.
+// Logits are compared exactly but for the dropped bits.
+template <int V, bool BIAS, bool GROUPS>
+__device__ __forceinline__ int route_quick(const float (&l)[V], const float (&b)[V], const float* row,
+                                           const float* __restrict__ bias, const RouteRow& q, float* mem, uint32_t* kp,
+                                           double* marks, bool& hard) {
+  constexpr uint32_t kPlace = V - 1;
+  const int lane = q.lane, E = q.E;
+  const bool soft = q.a.score == kScoreSoftmax;
+  const bool by_score = BIAS || (GROUPS && q.a.group_score == kGroupTop2);
+  float s[V];
+  if (by_score) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      s[j] = soft ? __expf(l[j] - q.top) : __builtin_amdgcn_rcpf(1.0f + __expf(-l[j]));
+      if (lane * V + j < E) sum += s[j];
+    }
+    if (soft) {
+      const float inv = __builtin_amdgcn_rcpf(lane_sum(sum));
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[j] *= inv;
+    }
+  }
+  uint32_t key[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (BIAS) s[j] += b[j];
+    key[j] = lane * V + j >= E ? 0u : (order_key(BIAS ? s[j] : l[j]) & ~kPlace) | (kPlace - j) | (V == 1 ? 1u : 0u);
+  }
+  if constexpr (GROUPS) {
+    const int per = E / q.a.n_groups;
+    if (lane < kMaxExperts / 32) kp[lane] = 0;
+    bool unclear = false;
+    float mk[V];
+    group_marks<V>(q, by_score ? s : l, mem, mk);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int g = lane + kRL * j;
+      if (kRL * j >= q.a.n_groups) break;
+      if (g < q.a.n_groups) {
+        // groups that may be, and that surely are, ahead of this one
+        const float thr = by_score ? (soft ? 0x1p-17f : 0x1p-19f) * (1.0f + fabsf(mk[j])) : 0.0f;
+        int may = 0, sure = 0;
+        for (int o = 0; o < q.a.n_groups; ++o) {
+          if (o == g) continue;
+          const float gap = mem[o] - mk[j];
+          may += !(gap < -thr || (!by_score && gap == 0.0f && o > g));
+          sure += gap > thr || (!by_score && gap == 0.0f && o < g);
+        }
+        if (may < q.a.top_groups) atomicOr(&kp[g >> 5], 1u << (g & 31));
+        else if (sure < q.a.top_groups) unclear = true;
+      }
+    }
+    wave_sync();
+    if (row_vote(unclear)) hard |= !close_groups<V>(s, row, BIAS ? bias : nullptr, q, mem, kp, marks);
+    int g = lane * V / per, in = lane * V - g * per;   // group of the lane's first expert and its place there
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (lane * V + j < E && !((kp[g >> 5] >> (g & 31)) & 1u)) key[j] = 0;
+      if (++in == per) {
+        in = 0;
+        ++g;
+      }
+    }
+  }
+  // Rounds: candidate k to lane k, until a certain gap behind the K-th.
+  int chosen = 0, count = 0;   // count: candidates of a finished list
+  bool sorted = true;          // the list's order is certain
+  uint32_t before = 0;
+  for (int k = 0; k <= kRL; ++k) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) best = max(best, key[j]);
+    const uint32_t m = lane_max(best);
+    const int first = __ffs(row_vote(best == m)) - 1;
+    const uint32_t now = m & ~kPlace;
+    const float hi = key_value(before), lo = key_value(now);
+    const bool clear = m == 0 || (BIAS ? hi - lo > 0x1p-18f * (1.0f + fabsf(hi)) : before != now);
+    if (count == 0 && k > 0) {
+      if (k >= q.K && clear) count = k;
+      else sorted &= clear;
+    }
+    if (__all(count != 0) || k == kRL) break;
+    if (lane == k) chosen = first * V + (int)(kPlace - (m & kPlace));
+    before = now;
+    const uint32_t taken = lane == first ? m : 0xffffffffu;   // (no key of a number)
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = key[j] == taken ? 0u : key[j];
+  }
+  if (count < q.K) hard = true;   // no end in 16, or fewer than K left
+  if (__any(!sorted && count > 0)) {
+    // the candidates' exact order: larger choice, then lower index
+    double den = 1.0;
+    if (BIAS && soft) {
+      den = 0.0;
+#pragma unroll 1
+      for (int e = lane * V; e < min(lane * V + V, E); ++e) den += exact_score(true, row[e], q.top);
+      den = lane_sum(den);
+    }
+    const bool have = lane < count;
+    const int e = have ? chosen : 0;
+    const unsigned long long mine =
+        !have ? 0ull
+              : BIAS ? order_key(exact_score(soft, row[e], q.top) / den + (double)bias[e])
+                     : (unsigned long long)order_key(row[e]);
+    int rank = 0;
+#pragma unroll 1
+    for (int o = 0; o < kRL; ++o) {
+      const unsigned long long other = __shfl(mine, o, kRL);
+      const int oe = __shfl(e, o, kRL);
+      rank += other > mine || (other == mine && other != 0 && oe < e);
+    }
+    int* at = reinterpret_cast<int*>(mem);
+    wave_sync();
+    if (have) at[rank] = e;
+    wave_sync();
+    if (have) chosen = at[lane];
+  }
+  return chosen;
+}
+
+// BIAS: a bias is given; GROUPS: more than one group.
+template <int V, bool BIAS, bool GROUPS, bool VEC>
+__global__ __launch_bounds__(256) void score_route_kernel(const float* __restrict__ logits,
+                                                          const float* __restrict__ bias, int64_t n, int E, int K,
+                                                          RouteArgs a, int32_t* __restrict__ topk,
+                                                          float* __restrict__ weights, int32_t* __restrict__ iota,
+                                                          int* __restrict__ status, int layer, int has_layer) {
+  __shared__ double member[kRTokens * kRL * V];
+  __shared__ uint32_t keep[GROUPS ? kRTokens * (kMaxExperts / 32) : 1];
+  __shared__ double marks[GROUPS ? kRTokens * kRL : 1];
+  const int lane = threadIdx.x % kRL, slot = threadIdx.x / kRL;
+  const int64_t t = (int64_t)blockIdx.x * kRTokens + slot;
+  const float* row = logits + (t < n ? t : n - 1) * E;   // tokens past the end repeat the last one
+  float l[V], b[V];
+  bool bad = false;
+  float top = -INFINITY;
+  if constexpr (VEC && V >= 4) {   // E a multiple of 4, rows 16-byte aligned
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 v = lane * V + j < E ? *reinterpret_cast<const float4*>(row + lane * V + j) : float4{0, 0, 0, 0};
+      l[j] = v.x;
+      l[j + 1] = v.y;
+      l[j + 2] = v.z;
+      l[j + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) l[j] = lane * V + j < E ? row[lane * V + j] : 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int e = lane * V + j;
+    b[j] = BIAS && e < E ? bias[e] : 0.0f;
+    bad |= !isfinite(l[j]) || !isfinite(b[j]);
+    if (e < E) top = fmaxf(top, l[j]);
+  }
+  top = lane_max(top);
+  const RouteRow q{E, K, lane, top, a};
+  double* mem = member + slot * kRL * V;
+  uint32_t* kp = keep + (GROUPS ? slot * (kMaxExperts / 32) : 0);
+  bool hard = false;
+  int chosen = route_quick<V, BIAS, GROUPS>(l, b, row, bias, q, reinterpret_cast<float*>(mem), kp,
+                                              GROUPS ? marks + slot * kRL : nullptr, hard);
+  if (__any(hard))
+    chosen = route_exact<V>(row, BIAS ? bias : nullptr, q, mem, GROUPS ? marks + slot * kRL : nullptr);
   // weights, in 64 bits: one chosen expert per lane
+  const bool soft = a.score == kScoreSoftmax;
   const bool mine = lane < K;
   const float lc = row[mine ? chosen : 0];
-  double w = 0.0;
-  if (soft && a.renormalize) {
-    // the softmax's own sum cancels; relative to the largest chosen logit nothing underflows to 0/0
-    const float lm = lane_max(mine ? lc : -INFINITY);
-    w = mine ? exp((double)lc - (double)lm) : 0.0;
-  } else if (mine) {
-    w = soft ? exp((double)lc - (double)top) / den : 1.0 / (1.0 + exp(-(double)lc));
+  // a renormalized softmax's own sum cancels; relative to the largest chosen logit nothing
+  // underflows to 0/0
+  const float ref = soft && a.renormalize ? lane_max(mine ? lc : -INFINITY) : top;
+  double w = mine ? exact_score(soft, lc, ref) : 0.0;
+  if (soft && !a.renormalize) {
+    float sum = 0.0f;   // of at most 16 per lane: a double from there on
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum += lane * V + j < E ? expf(l[j] - top) : 0.0f;
+    w /= lane_sum((double)sum);
   }
   if (a.renormalize) {
     const double sum = lane_sum(w);
@@ -227,11 +513,15 @@ struct RouteCall {
   int layer, has_layer;
 };
 
-template <int V, bool WIDE, bool GROUPS>
+template <int V, bool BIAS, bool GROUPS>
 void run_route(const RouteCall& c, hipStream_t s) {
-  hipLaunchKernelGGL((score_route_kernel<V, WIDE, GROUPS>), dim3((unsigned)((c.n + kRTokens - 1) / kRTokens)),
-                     dim3(256), 0, s, c.logits, c.bias, c.n, c.E, c.K, c.a, c.topk, c.weights, c.iota, c.status,
-                     c.layer, c.has_layer);
+  const dim3 grid((unsigned)((c.n + kRTokens - 1) / kRTokens)), block(256);
+  if (c.E % 4 == 0 && reinterpret_cast<uintptr_t>(c.logits) % 16 == 0)
+    hipLaunchKernelGGL((score_route_kernel<V, BIAS, GROUPS, true>), grid, block, 0, s, c.logits, c.bias, c.n, c.E, c.K,
+                       c.a, c.topk, c.weights, c.iota, c.status, c.layer, c.has_layer);
+  else
+    hipLaunchKernelGGL((score_route_kernel<V, BIAS, GROUPS, false>), grid, block, 0, s, c.logits, c.bias, c.n, c.E, c.K,
+                       c.a, c.topk, c.weights, c.iota, c.status, c.layer, c.has_layer);
 }
 template <int V>
 void run_route_v(const RouteCall& c, hipStream_t s) {

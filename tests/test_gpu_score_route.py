@@ -86,6 +86,31 @@ def test_equal_close_and_extreme_logits(score, biased):
                group_score="top2")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("E,groups,top", [(64, 8, 3), (256, 8, 4), (96, 4, 2), (128, 64, 5), (40, 5, 2)])
+def test_groups_and_choices_next_to_each_other(score, group_score, E, groups, top):
+    """Groups whose marks differ by a few units in the last place or not at all, with distinct members and
+    with close ones; lists of close choices longer and shorter than the 16 lanes of a token."""
+    rng = np.random.default_rng(E + groups)
+    per, K, n = E // groups, 6 if top * (E // groups) >= 6 else top * (E // groups), 120
+    l = rng.normal(-2.0, 0.7, (n, E)).astype(np.float32)
+    for t in range(n):
+        v = l[t].reshape(groups, per)
+        if t % 3 < 2:                                     # the same largest members in every group, moved a little
+            big = np.float32(1.5) + np.arange(min(per, 2), dtype=np.float32) * np.float32(0.25)
+            v[:, :big.size] = big
+            v[:, 0] += rng.integers(0, 3, groups) * np.float32(2.0 ** -22) * (t % 3)
+            rng.shuffle(v, axis=1)
+        else:                                             # everything close
+            v[:] = np.float32(0.5) + rng.integers(0, 6, (groups, per)) * np.float32(2.0 ** -23)
+    bias = (rng.integers(0, 2, E) * np.float32(0.125)).astype(np.float32)
+    ctx = _ctx(E, K)
+    for b in (None, bias, np.zeros(E, np.float32)):
+        _check(ctx, l, K, score=score, bias=b, groups=groups, top_groups=top, group_score=group_score)
+        _check(ctx, l, K, score=score, bias=b)
+
+
 def test_many_tokens_and_optional_outputs():
     E, K, n = 256, 8, 40961
     rng = np.random.default_rng(3)
