@@ -107,14 +107,16 @@ __global__ __launch_bounds__(T::kThreads) void mx_matmul_tile_kernel(const uint8
   const int nl = n - 1 - n0, ml = (int)min(m - 1 - m0, (int64_t)T::TM);
   const MxOperand W{w + (int64_t)n0 * nb * kMxBlockBytes, ws + (int64_t)n0 * nb};
   const MxOperand X{a + m0 * nb * kMxBlockBytes, as + m0 * nb};
-  mx_tile_products<T, WORDS>(W, X, [&](int r) { return min(r, nl); }, [&](int r) { return min(r, ml); }, nb, MX_TILE_ARGS, acc);
-  mx_meet<0>();   // the buffers becomes the waves' output regions
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t wm0 = m0 + wave % T::WM * T::FM * 32;
-  const int wn0 = n0 + wave / T::WM * T::FN * 32;
+  const int64_t wm0 = m0 + mx_wave_m<T>(wave) * T::FM * 32;
+  const int wn0 = n0 + mx_wave_n<T>(wave) * T::FN * 32;
+  mx_tile_products<T, WORDS>(W, X, [&](int r) { return min(r, nl); }, [&](int r) { return min(r, ml); }, nb,
+                             wm0 < m && wn0 < n, MX_TILE_ARGS, acc);
+  mx_meet<0>();   // the buffers becomes the waves' output regions
   char* region = mx_region<T>(wave, MX_TILE_ARGS);
   if (bf16)
-    mx_tile_rows_bf16<T>(region, acc, [&](int row, int col, uint4 v) {
+    mx_tile_rows16<T>(region, [&](int i, int j, uint2 (&h)[4]) { mx_pack_bf16(acc[i][j], h); },
+                      [&](int row, int col, uint4 v) {
       if (wm0 + row < m && wn0 + col < n) mx_put8(static_cast<uint16_t*>(out), wm0 + row, n, wn0 + col, v);
     });
   else

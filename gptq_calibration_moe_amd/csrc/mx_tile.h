@@ -51,6 +51,13 @@ struct MxTile {
   static constexpr int kBufBytes = kRows * kStageBytes;
 };
 
+// A wave's place in the tile.  The waves of one matrix core (wave % 4) are far apart in
+// rows of x, so that a tile whose last rows are missing leaves every core its share.
+template <class T>
+__device__ __forceinline__ int mx_wave_n(int wave) { return wave % T::WN; }
+template <class T>
+__device__ __forceinline__ int mx_wave_m(int wave) { return wave / T::WN; }
+
 // LDS of a tile in a kernel: two stages' codes and two pairs of stages' scales.
 #define MX_TILE_LDS(T)                                                                     \
   __shared__ __attribute__((aligned(1024))) char mx_b0[T::kBufBytes], mx_b1[T::kBufBytes]; \
@@ -81,13 +88,14 @@ struct MxOperand {
 // (0 .. TN-1, 0 .. TM-1), always one that exists and less than 2^32 bytes from the
 // base.  The buffers are separate arrays so that the compiler can tell a stage being
 // loaded from one being read.  WORDS: nb is a multiple of 4, at least 16.
-// acc[FN][FM] += the tile's products over nb blocks.
+// acc[FN][FM] += the tile's products over nb blocks; a wave that is not active (none of
+// its rows exist) only takes part in the loading.
 template <class T, bool WORDS, class WRow, class XRow>
 __device__ __forceinline__ void mx_tile_products(const MxOperand& W, const MxOperand& X, WRow&& wrow_of, XRow&& xrow_of,
-                                                 int nb, char* b0, char* b1, uint4* sc,
+                                                 int nb, bool active, char* b0, char* b1, uint4* sc,
                                                  f32x16 (&acc)[T::FN][T::FM]) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wn = wave / T::WM, wm = wave % T::WM;
+  const int wn = mx_wave_n<T>(wave), wm = mx_wave_m<T>(wave);
   const int stages = (nb + kStageBlocks - 1) / kStageBlocks, full = nb / kStageBlocks;
   // load i of this wave fills tile rows 8 (kWaves i + wave) .. + 7; the block that lands in slot lane % 8 of row lane / 8
   const int piece = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
@@ -204,6 +212,14 @@ __device__ __forceinline__ void mx_tile_products(const MxOperand& W, const MxOpe
   // two stages go the next two's scales, which the second one publishes.
   auto turn = [&](int s, char* here, const char* there, const uint4* scales, uint4* other, auto half_) {
     constexpr int half = decltype(half_)::value;
+    if (!active) {
+      if constexpr (half == 1 && !WORDS) store_scales(other);
+      mx_meet<0>();
+      issue(s + 2, here);
+      if constexpr (half == 0 && WORDS) issue_scales(s + 2, other);
+      if constexpr (half == 0 && !WORDS) load_scales(s + 2);
+      return;
+    }
     fetch(here, 1);
     __builtin_amdgcn_sched_barrier(0);
     multiply(J0, half);
@@ -315,10 +331,12 @@ __device__ __forceinline__ void mx_tile_rows(char* region, const f32x16 (&acc)[T
     }
 }
 
-// bf16, 32 rows at a time: rounded before they go through LDS, which halves its
-// traffic (the epilogue's bound).  put(row, col, q): eight results.
-template <class T, class Put>
-__device__ __forceinline__ void mx_tile_rows_bf16(char* region, const f32x16 (&acc)[T::FN][T::FM], Put&& put) {
+// 16-bit results, 32 rows at a time: packed before they go through LDS, which halves
+// its traffic (the epilogue's bound).  pack(a, b, h): the halves of fragment (a, b) in
+// four 8-byte words, word q columns 8 q + 4 (lane / 32) + 0..3; put(row, col, v): eight
+// results.
+template <class T, class Pack, class Put>
+__device__ __forceinline__ void mx_tile_rows16(char* region, Pack&& pack, Put&& put) {
   constexpr int kGroups = 4 * T::FN;   // of 16 bytes in a row
   static_assert(32 * kGroups * 16 <= 8192 && (kGroups & (kGroups - 1)) == 0, "rows in the region, power of two");
   const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
@@ -327,13 +345,12 @@ __device__ __forceinline__ void mx_tile_rows_bf16(char* region, const f32x16 (&a
 #pragma unroll
   for (int b = 0; b < T::FM; ++b) {
 #pragma unroll
-    for (int a = 0; a < T::FN; ++a)
+    for (int a = 0; a < T::FN; ++a) {
+      uint2 h[4];
+      pack(a, b, h);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x16& v = acc[a][b];
-        half[2 * (r * kGroups + ((4 * a + q) ^ (r & (kGroups - 1)))) + g] =
-            make_uint2(mx_bf16_pair(v[4 * q], v[4 * q + 1]), mx_bf16_pair(v[4 * q + 2], v[4 * q + 3]));
-      }
+      for (int q = 0; q < 4; ++q) half[2 * (r * kGroups + ((4 * a + q) ^ (r & (kGroups - 1)))) + g] = h[q];
+    }
     __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
     for (int i = 0; i < kGroups / 2; ++i) {
@@ -342,6 +359,11 @@ __device__ __forceinline__ void mx_tile_rows_bf16(char* region, const f32x16 (&a
     }
     __builtin_amdgcn_wave_barrier();
   }
+}
+__device__ __forceinline__ void mx_pack_bf16(const f32x16& v, uint2 (&h)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    h[q] = make_uint2(mx_bf16_pair(v[4 * q], v[4 * q + 1]), mx_bf16_pair(v[4 * q + 2], v[4 * q + 3]));
 }
 
 }  // namespace clha

@@ -49,7 +49,8 @@ class Block:
         n = x.shape[0]
         terms = self.K + self.shared
         want, tol = oracle.mx_experts(x.double().cpu().numpy(), topk, w, self.gu_values, self.d_values, self.E,
-                                      sum_eps=max(self.d, self.f) * 2.0 ** -23)
+                                      sum_eps=max(self.d, self.f) * 2.0 ** -23,
+                                      pair_eps=2 / 65534 + 2.0 ** -23 if got.dtype == torch.bfloat16 else 0.0)
         tol = tol + terms * 2.0 ** -23 * (np.abs(want) + tol + 1.0 * np.abs(w).sum())
         tol = tol + (np.abs(want) + tol) * (2.0 ** -8 if got.dtype == torch.bfloat16 else 2.0 ** -24)
         g = got.double().cpu().numpy()
