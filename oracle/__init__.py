@@ -595,8 +595,10 @@ def mx_experts(x, topk, weights, wgu, wd, n_routed: int, sum_eps: float = 0.0, p
         g, u, eg, eu = gu[:, :f], gu[:, f:], err[:, :f], err[:, f:]
         sl = silu(g)
         h = sl * u
-        # |silu'| <= 1.1; exp, division and two products in fp32: 8 units in the last place
-        dh = 1.1 * eg * (np.abs(u) + eu) + np.abs(sl) * eu + (8 * 2.0 ** -24) * np.abs(h)
+        # |silu'| <= 1.1.  In fp32 1 / (1 + 2^(-g log2 e)): the constant and its product round by
+        # 2^-24 each, so 2^x is off by 2 |g| 2^-24 and its own 2 2^-24, which 1 / (1 + .) passes on
+        # by at most their whole; the sum rounds by 1, the reciprocal by 2, two products by 1 each
+        dh = 1.1 * eg * (np.abs(u) + eu) + np.abs(sl) * eu + (8 + 2 * np.abs(g)) * 2.0 ** -24 * np.abs(h)
         lo, hi = h - dh, h + dh
         top = lambda a: np.abs(a).reshape(t.size, -1, 32).max(axis=2)          # noqa: E731
         q = [mx_values(c[..., 0::2] | (c[..., 1::2] << 4), s)
