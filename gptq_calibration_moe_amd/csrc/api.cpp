@@ -1279,7 +1279,6 @@ static size_t experts_layout(const clha_ctx* ctx, int64_t n, int f, void* ws, Ex
   p.offsets = c.take<int32_t>((size_t)p.E);
   p.order = c.take<int32_t>((size_t)p.pairs);
   p.tiles = c.take<int32_t>((size_t)3 * p.max_tiles);
-  p.n_tiles = c.take<int32_t>(1);
   p.hq = c.take<uint8_t>((size_t)all * f / 2);
   p.hs = c.take<uint8_t>((size_t)all * f / 32);
   p.ypair = c.take<float>((size_t)all * d.d);

@@ -51,7 +51,7 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* wave_sum, int3
 // has slot e (slots <= kPlanThreads).  first[e] becomes the slot's first position.
 __device__ __forceinline__ void plan_tiles(const int32_t* cnt, int32_t* first, int32_t* wave_sum, int E, int slots,
                                            int32_t n, int32_t pairs, int rows, int32_t* __restrict__ tiles,
-                                           int32_t* __restrict__ n_tiles) {
+                                           int max_tiles) {
   const int e = threadIdx.x;
   const int32_t mine = e < E ? cnt[e] : e < slots ? n : 0;
   int32_t total;
@@ -59,7 +59,7 @@ __device__ __forceinline__ void plan_tiles(const int32_t* cnt, int32_t* first, i
   const int32_t pos = e < E ? off : pairs + (e - E) * n;
   const int32_t tile0 = block_scan((mine + rows - 1) / rows, wave_sum, &total);
   if (e < E) first[e] = pos;
-  if (threadIdx.x == 0) *n_tiles = total;
+  for (int i = total + threadIdx.x; i < max_tiles; i += kPlanThreads) tiles[3 * (int64_t)i + 2] = 0;   // no tile
   for (int i = 0; i * rows < mine; ++i) {
     int32_t* d = tiles + 3 * (int64_t)(tile0 + i);
     d[0] = e;
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kPlanThreads) void experts_begin_kernel(ExpertsPlan
     return;
   }
   count_pairs(p.topk, 0, p.pairs, p.E, cnt);
-  plan_tiles(cnt, first, wave_sum, p.E, p.E + p.shared, p.n, p.pairs, p.tile_rows, p.tiles, p.n_tiles);
+  plan_tiles(cnt, first, wave_sum, p.E, p.E + p.shared, p.n, p.pairs, p.tile_rows, p.tiles, p.max_tiles);
   place_pairs(p.topk, 0, p.pairs, p.E, first, p.order);
 }
 
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kPlanThreads) void experts_scan_kernel(ExpertsPlan 
     if (part) cnt[e] = before + sum;
   }
   __syncthreads();
-  plan_tiles(cnt, first, wave_sum, p.E, p.E + p.shared, p.n, p.pairs, p.tile_rows, p.tiles, p.n_tiles);
+  plan_tiles(cnt, first, wave_sum, p.E, p.E + p.shared, p.n, p.pairs, p.tile_rows, p.tiles, p.max_tiles);
   for (int i = threadIdx.x; i < p.E; i += kPlanThreads) p.offsets[i] = first[i];
 }
 
@@ -219,9 +219,9 @@ __device__ __forceinline__ void experts_h(const ExpertsPlan& p, const f32x4 (&pa
 template <int MF, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void experts_up_stream_kernel(ExpertsPlan p) {
   __shared__ f32x4 part[WAVES][4 * MF][64];
-  if ((int)blockIdx.x >= *p.n_tiles) return;
   const int32_t* td = p.tiles + 3 * (int64_t)blockIdx.x;
   const int e = td[0], pos0 = td[1], rows = td[2];
+  if (rows == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
   const int f0 = blockIdx.y * 32;
   const int nb = p.d / kMxBlock;
@@ -254,9 +254,9 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_stream_kernel(ExpertsPl
 template <int MF, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void experts_down_stream_kernel(ExpertsPlan p) {
   __shared__ f32x4 part[WAVES][MF][64];
-  if ((int)blockIdx.x >= *p.n_tiles) return;
   const int32_t* td = p.tiles + 3 * (int64_t)blockIdx.x;
   const int e = td[0], pos0 = td[1], rows = td[2];
+  if (rows == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
   const int c0 = blockIdx.y * 16;
   const int nb = p.f / kMxBlock;
@@ -364,17 +364,22 @@ __global__ __launch_bounds__(64 * WAVES) void experts_down_few_kernel(ExpertsPla
 
 // ------------------------------------------------------------------ products over many positions
 // One tile of mx_tile.h per workgroup: TM positions of a tile of the plan by TN rows
-// of W.  Workgroup b runs on die b % kXcds; a die takes a contiguous run of the
-// (position tile, row tile) pairs, row tiles fastest, so what it runs together is a few
-// position tiles of one slot against all of that slot's weights, which its L2 holds.
+// of W.  Workgroup b runs on die b % kXcds.  The dies take groups of four position
+// tiles in turn (whatever the number of tiles, which only the device knows, they share
+// them evenly), row tiles fastest: what a die runs together is about one group against all
+// of its slot's weights, which its L2 holds.
+constexpr int kTileGroup = 4;
 struct TileAt {
   int tile, part;
-  bool any;
 };
-__device__ __forceinline__ TileAt experts_tile_at(const ExpertsPlan& p, int parts) {
-  const int64_t total = (int64_t)*p.n_tiles * parts, per = (total + kXcds - 1) / kXcds;
-  const int64_t i = blockIdx.x / kXcds, L = (int64_t)(blockIdx.x % kXcds) * per + i;
-  return {(int)(L / parts), (int)(L % parts), i < per && L < total};
+__device__ __forceinline__ TileAt experts_tile_at(int parts) {
+  const int per = kTileGroup * parts, i = blockIdx.x / kXcds;
+  const int in = i % per;
+  return {(i / per * kXcds + (int)(blockIdx.x % kXcds)) * kTileGroup + in / parts, in % parts};
+}
+int64_t experts_tile_grid(int64_t max_tiles, int parts) {
+  const int64_t groups = (max_tiles + kTileGroup - 1) / kTileGroup;
+  return (groups + kXcds - 1) / kXcds * kXcds * kTileGroup * parts;
 }
 
 // First product: a wave's rows of W are FN/2 fragments of gate rows and the up rows
@@ -384,10 +389,11 @@ template <class T, bool WORDS>
 __global__ __launch_bounds__(T::kThreads) void experts_up_tile_kernel(ExpertsPlan p) {
   MX_TILE_LDS(T);
   constexpr int kFeatures = T::TN / 2, kWaveFeatures = kFeatures / T::WN;
-  const TileAt at = experts_tile_at(p, p.f / kFeatures);
-  if (!at.any) return;
+  const TileAt at = experts_tile_at(p.f / kFeatures);
+  if (at.tile >= p.max_tiles) return;
   const int32_t* td = p.tiles + 3 * (int64_t)at.tile;
   const int e = td[0], pos0 = td[1], rows = td[2];
+  if (rows == 0) return;
   const int f0 = at.part * kFeatures, nb = p.d / kMxBlock, hb = p.f / kMxBlock;
   const MxOperand W{p.wgu + (int64_t)e * 2 * p.f * nb * kMxBlockBytes, p.wgu_scales + (int64_t)e * 2 * p.f * nb};
   const MxOperand X{p.xq, p.xs};
@@ -471,10 +477,11 @@ template <class T, bool WORDS, bool SHORT>
 __global__ __launch_bounds__(T::kThreads) void experts_down_tile_kernel(ExpertsPlan p) {
   MX_TILE_LDS(T);
   const int parts = (p.d + T::TN - 1) / T::TN;
-  const TileAt at = experts_tile_at(p, parts);
-  if (!at.any) return;
+  const TileAt at = experts_tile_at(parts);
+  if (at.tile >= p.max_tiles) return;
   const int32_t* td = p.tiles + 3 * (int64_t)at.tile;
   const int e = td[0], pos0 = td[1], rows = td[2];
+  if (rows == 0) return;
   const int c0 = at.part * T::TN, nb = p.f / kMxBlock;
   const MxOperand W{p.wd + ((int64_t)e * p.d + c0) * nb * kMxBlockBytes, p.wd_scales + ((int64_t)e * p.d + c0) * nb};
   const MxOperand X{p.hq + (int64_t)pos0 * nb * kMxBlockBytes, p.hs + (int64_t)pos0 * nb};
@@ -575,9 +582,9 @@ constexpr int64_t kFewPairs = 32;
 namespace {
 template <class T, bool UP, bool DOWN>   // whether the rows' scales of each product are whole words
 void run_tiles(const ExpertsPlan& p, bool bf16, hipStream_t s) {
-  const int64_t up = (int64_t)p.max_tiles * (p.f / (T::TN / 2)), down = (int64_t)p.max_tiles * ((p.d + T::TN - 1) / T::TN);
-  const dim3 block(T::kThreads), down_grid((unsigned)((down + kXcds - 1) / kXcds * kXcds));
-  hipLaunchKernelGGL((experts_up_tile_kernel<T, UP>), dim3((unsigned)((up + kXcds - 1) / kXcds * kXcds)), block, 0, s, p);
+  const dim3 block(T::kThreads), up_grid((unsigned)experts_tile_grid(p.max_tiles, p.f / (T::TN / 2))),
+      down_grid((unsigned)experts_tile_grid(p.max_tiles, (p.d + T::TN - 1) / T::TN));
+  hipLaunchKernelGGL((experts_up_tile_kernel<T, UP>), up_grid, block, 0, s, p);
   if (bf16) hipLaunchKernelGGL((experts_down_tile_kernel<T, DOWN, true>), down_grid, block, 0, s, p);
   else hipLaunchKernelGGL((experts_down_tile_kernel<T, DOWN, false>), down_grid, block, 0, s, p);
 }
