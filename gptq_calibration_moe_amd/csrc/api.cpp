@@ -597,6 +597,7 @@ CLHA_API clha_status clha_collect_hessians_scored(clha_ctx* ctx, int32_t layer, 
   if (!ctx) return CLHA_ERR_INVALID_ARG;
   const clha_status st = check_route(ctx, "collect_hessians_scored", desc, n_tokens);
   if (st != CLHA_OK) return st;
+  const OnDevice on(ctx);
   return collect(ctx, "collect_hessians_scored", Scored{desc, bias, weights_out}, layer, n_tokens, x, logits, topk_out,
                  offsets_out, token_ids_out, workspace, workspace_bytes, stream);
 }
@@ -1245,7 +1246,7 @@ CLHA_API clha_status clha_mx_matmul(clha_ctx* ctx, int64_t m, int32_t n, int32_t
   if (k < 32 || k > clha::kMaxMxK || k % 32 != 0)
     return fail(ctx, CLHA_ERR_SHAPE, "mx_matmul: k %d is not a multiple of 32 in 32..%d", k, clha::kMaxMxK);
   if (n < 1 || n > clha::kMaxMxN) return fail(ctx, CLHA_ERR_SHAPE, "mx_matmul: n %d outside 1..%d", n, clha::kMaxMxN);
-  if (m < 0 || m > INT32_MAX || m > ((int64_t)1 << 40) / n)
+  if (m < 0 || m > clha::kMaxMxM || m > clha::kMaxMxResults / n)
     return fail(ctx, CLHA_ERR_SHAPE, "mx_matmul: m %lld is out of range", (long long)m);
   if (out_dtype != CLHA_F32 && out_dtype != CLHA_BF16) return fail(ctx, CLHA_ERR_INVALID_ARG, "mx_matmul: bad dtype");
   if (m == 0) return CLHA_OK;
@@ -1288,8 +1289,10 @@ static size_t experts_layout(const clha_ctx* ctx, int64_t n, int f, void* ws, Ex
 
 static bool experts_sizes(const clha_ctx* ctx, int64_t n, int32_t f) {
   const clha_moe_desc& d = ctx->desc;
-  return n >= 0 && n <= d.max_tokens && d.n_shared <= clha::kMaxShared &&
-         n <= clha::kMaxExpertPairs / (d.top_k + d.n_shared) && n <= clha::kMaxExpertValues / d.d && f >= 128 && f <= 8192 && f % 128 == 0;
+  const int64_t each = d.top_k + d.n_shared;
+  return n >= 0 && n <= d.max_tokens && d.n_shared <= clha::kMaxShared && f >= 128 && f <= 8192 && f % 128 == 0 &&
+         n <= clha::kMaxExpertPairs / each && n <= clha::kMaxExpertWork / (each * std::max(d.d, f)) &&
+         n <= clha::kMaxExpertValues / d.d;
 }
 
 CLHA_API size_t clha_mx_experts_workspace_bytes(const clha_ctx* ctx, int64_t n_tokens, int32_t f) {

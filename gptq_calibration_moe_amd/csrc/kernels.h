@@ -218,6 +218,10 @@ void launch_score_route(const float* logits, const float* bias, int64_t n, int E
 constexpr int64_t kMaxMxValues = (int64_t)1 << 34;   // values of one quantize / dequantize call
 constexpr int kMaxMxK = 65536;                       // contraction length of a product
 constexpr int kMaxMxN = 524288;                      // rows of its right operand
+// Rows of the left operand and results: a launch counts its threads in 32 bits, and
+// (m/128 + 1) (n/128 + 1) 256 stays below 2^32.
+constexpr int64_t kMaxMxM = (int64_t)1 << 30;
+constexpr int64_t kMaxMxResults = (int64_t)1 << 36;
 void launch_mx_quantize(const void* x, bool bf16, int64_t rows, int cols, int64_t ld, uint8_t* codes, uint8_t* scales,
                         hipStream_t s);
 void launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, void* out, bool bf16,
@@ -229,6 +233,8 @@ void launch_mx_matmul(const uint8_t* a, const uint8_t* as, const uint8_t* w, con
 constexpr int kMaxShared = 256;                            // shared experts of one pass
 constexpr int kMaxExpertSlots = kMaxExperts + kMaxShared;  // routed and shared experts
 constexpr int64_t kMaxExpertPairs = (int64_t)1 << 27;      // (token, expert) pairs of one pass
+// pairs x the wider of d and f, for the same reason: (pairs/128 + 544) (f/64) 256 threads.
+constexpr int64_t kMaxExpertWork = (int64_t)1 << 36;
 constexpr int64_t kMaxExpertValues = (int64_t)1 << 33;     // values of x of one pass: its codes stay within 32-bit offsets
 struct ExpertsPlan {
   int32_t n, d, f, E, K, shared;

@@ -188,8 +188,8 @@ CLHA_API clha_status clha_route(clha_ctx* ctx, const clha_route_desc* desc, int6
                                 const float* bias, int32_t* topk_out, float* weights_out, void* stream);
 
 /* clha_collect_hessians for a block that routes by scores: step 1 is clha_route's choice (with its
- * optional weights); everything else is as documented there, the workspace included.  A non-finite
- * bias is latched like a logit. */
+ * optional weights); everything else is as documented there, the workspace included, with n_tokens
+ * at most 2^27 as well.  A non-finite bias is latched like a logit. */
 CLHA_API clha_status clha_collect_hessians_scored(clha_ctx* ctx, int32_t layer, const clha_route_desc* desc,
                                                   int64_t n_tokens, const uint16_t* x, const float* logits,
                                                   const float* bias, int32_t* topk_out, float* weights_out,
@@ -435,7 +435,7 @@ CLHA_API clha_status clha_mx_dequantize(clha_ctx* ctx, int64_t rows, int32_t col
  *   a   [m][k], w [n][k] in MXFP4; m >= 0, n 1..524288, k a multiple of 32, 32..65536
  *   out device, [m][n] fp32 or bf16 (out_dtype), 16-byte aligned
  * A NaN block makes the row (of a) or column (of w) NaN.  m == 0 enqueues nothing and reads no
- * pointer.  m * n at most 2^40, m at most 2^31 - 1.
+ * pointer.  m * n at most 2^36, m at most 2^30.
  * Errors: INVALID_ARG, SHAPE, ALIGN, HIP. */
 CLHA_API clha_status clha_mx_matmul(clha_ctx* ctx, int64_t m, int32_t n, int32_t k, const uint8_t* a,
                                     const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales, void* out,
@@ -451,8 +451,8 @@ CLHA_API size_t clha_mx_experts_workspace_bytes(const clha_ctx* ctx, int64_t n_t
  *   y_t = sum_k weights[t][k] (hq Wd_e^T), e = topk[t][k], in the order of k, then the shared
  *         experts' with weight 1 (fp32); one rounding to the output type.
  * MX(.) is clha_mx_quantize.
- *   x        device, bf16 bits [n_tokens][d]; n_tokens 0..max_tokens, at most 2^27 / (K + n_shared)
- *            and 2^33 / d
+ *   x        device, bf16 bits [n_tokens][d]; n_tokens 0..max_tokens, at most 2^33 / d; the pairs
+ *            n_tokens (K + n_shared) at most 2^27 and 2^36 / max(d, f)
  *   topk     device, int32 [n_tokens][K]; an id outside 0..E-1 stands for no expert and adds
  *            nothing; the same expert twice counts twice
  *   weights  device, float [n_tokens][K]
@@ -460,6 +460,10 @@ CLHA_API size_t clha_mx_experts_workspace_bytes(const clha_ctx* ctx, int64_t n_t
  *   wd       [E + n_shared][d][f] in MXFP4
  *   f        multiple of 128, 128..8192; n_shared at most 256
  *   out      device, [n_tokens][d] fp32 or bf16 (out_dtype), 16-byte aligned
+ * fp32 sums; silu(g) u is within (8 + 2 |g|) 2^-24 of its value (beyond it |g u| 2^-126).  With bf16
+ * outputs and many tokens per expert the pairs' y_pair are held in 16 bits with an exponent per 32
+ * features, off by at most 2^-15 of the largest of them; a block of 32 that holds a NaN or an
+ * infinity becomes NaN.
  * Results do not depend on timing.  Calls that share a workspace must be ordered on one stream.
  * Errors: INVALID_ARG, SHAPE, ALIGN, WORKSPACE, HIP.  n_tokens == 0 enqueues nothing and reads
  * no pointer. */

@@ -240,3 +240,19 @@ def test_refusals(ctx):
         ctx.mx_matmul(codes, scales, *ctx.mx_quantize(torch.zeros(4, 96, device=dev())))
     with pytest.raises(clha.ClhaError):
         ctx.mx_quantize(x[:1].expand(4, 64))
+
+
+def test_products_beyond_one_launch_are_refused(ctx):
+    """A launch counts its threads in 32 bits: 256 for a tile of 128 x 128 results, so
+    m rows of one column need m / 128 * 256 of them."""
+    import gptq_calibration_moe_amd as clha
+    t = torch.zeros(64, dtype=torch.uint8, device=dev())
+    p = t.data_ptr()
+    for m, n in (((1 << 30) + 1, 1), (1 << 31, 1), ((1 << 26) + 1, 1024), ((1 << 17) + 1, 524288)):
+        st = clha.lib.clha_mx_matmul(ctx._h, m, n, 32, p, p, p, p, p, clha.F32, None)
+        assert st == clha.ERR_SHAPE, (m, n)
+    for tile, threads in ((128, 256), (256, 512)):   # the largest calls that are taken
+        for m in (129, 1 << 17, 1 << 20, 1 << 26, 1 << 30):
+            n = min((1 << 36) // m, 524288)
+            tiles = -(-m // tile) * -(-n // tile)
+            assert (tiles + 7) // 8 * 8 * threads < 1 << 32

@@ -223,3 +223,21 @@ def test_other_stages_are_timed():
     t = b.ctx.read_timing()
     b.ctx.set_timing(False)
     assert t["mx_experts"][1] == 1 and t["mx_quantize"][1] == 1 and t["mx_experts"][0] > 0
+
+
+@pytest.mark.parametrize("d,f", [(128, 8192), (8192, 128), (2048, 1408)])
+def test_passes_beyond_one_launch_are_refused(d, f):
+    """Threads of a launch are counted in 32 bits: the pairs times the wider of d and f
+    end at 2^36."""
+    import gptq_calibration_moe_amd as clha
+    ctx = clha.Context(d, 4, 2, 1, 1 << 27)
+    most = min((1 << 27) // 3, (1 << 36) // (3 * max(d, f)), (1 << 33) // d)
+    assert ctx.mx_experts_workspace_bytes(most, f) > 0
+    assert ctx.mx_experts_workspace_bytes(most + 1, f) == 0
+    t = torch.zeros(64, dtype=torch.uint8, device=dev())
+    p = t.data_ptr()
+    st = clha.lib.clha_mx_experts(ctx._h, most + 1, f, p, p, p, p, p, p, p, p, clha.F32, p, 64, None)
+    assert st == clha.ERR_SHAPE
+    for tile, threads in ((128, 256), (256, 512)):
+        tiles = 3 * most // tile + 4 + 1 + 32
+        assert tiles * (f // (tile // 2)) * threads < 1 << 32 and tiles * -(-d // tile) * threads < 1 << 32
