@@ -75,21 +75,13 @@ __device__ __forceinline__ uint32_t mx_codes8(const float* v, int scale_byte) {
   return q;
 }
 
-// Eight bf16 values at v (chunk i of a run of whole blocks): codes and scales, four
+// Eight values v, chunk i of a run of whole blocks: codes and scales, four
 // neighbouring lanes per block.
-__device__ __forceinline__ void mx_quantize8(const uint16_t* v, int64_t i, uint8_t* codes, uint8_t* scales) {
-  const uint4 q = *reinterpret_cast<const uint4*>(v);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  float f[8];
+__device__ __forceinline__ void mx_quantize8(const float (&v)[8], int64_t i, uint8_t* codes, uint8_t* scales) {
   uint32_t m = 0;   // magnitudes compare as their bits; NaN and infinity are the largest
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f[2 * j] = __uint_as_float(w[j] << 16);
-    f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-  }
-#pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t u = __float_as_uint(f[j]) & 0x7fffffffu;
+    const uint32_t u = __float_as_uint(v[j]) & 0x7fffffffu;
     m = u > m ? u : m;
   }
 #pragma unroll
@@ -98,8 +90,19 @@ __device__ __forceinline__ void mx_quantize8(const uint16_t* v, int64_t i, uint8
     m = u > m ? u : m;
   }
   const int sb = mx_scale_byte(m);
-  reinterpret_cast<uint32_t*>(codes)[i] = sb == kMxNan ? 0u : mx_codes8(f, sb);
+  reinterpret_cast<uint32_t*>(codes)[i] = sb == kMxNan ? 0u : mx_codes8(v, sb);
   if ((i & 3) == 0) scales[i >> 2] = (uint8_t)sb;
+}
+__device__ __forceinline__ void mx_quantize8(const uint16_t* x, int64_t i, uint8_t* codes, uint8_t* scales) {   // bf16
+  const uint4 q = *reinterpret_cast<const uint4*>(x);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  }
+  mx_quantize8(v, i, codes, scales);
 }
 
 }  // namespace clha

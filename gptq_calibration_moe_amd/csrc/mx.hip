@@ -13,8 +13,6 @@
 
 namespace clha {
 
-__device__ __forceinline__ float bf16_value(uint32_t b) { return __uint_as_float(b << 16); }
-
 template <bool BF16>
 __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict__ x, int64_t chunks, int row_chunks,
                                                           int64_t ld, uint8_t* __restrict__ codes,
@@ -23,35 +21,14 @@ __global__ __launch_bounds__(256) void mx_quantize_kernel(const void* __restrict
   if (i >= chunks) return;                                      // a block's four lanes leave together
   const int64_t r = i / row_chunks;
   const int64_t at = r * ld + 8 * (i - r * row_chunks);
-  float v[8];
   if constexpr (BF16) {
-    const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = bf16_value(w[j] & 0xffffu);
-      v[2 * j + 1] = bf16_value(w[j] >> 16);
-    }
+    mx_quantize8(static_cast<const uint16_t*>(x) + at, i, codes, scales);
   } else {
     const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
     const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    mx_quantize8(v, i, codes, scales);
   }
-  uint32_t m = 0;   // magnitudes compare as their bits; NaN and infinity are the largest
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t u = __float_as_uint(v[j]) & 0x7fffffffu;
-    m = u > m ? u : m;
-  }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    const uint32_t u = __shfl_xor(m, o);
-    m = u > m ? u : m;
-  }
-  const int sb = mx_scale_byte(m);
-  reinterpret_cast<uint32_t*>(codes)[i] = sb == kMxNan ? 0u : mx_codes8(v, sb);
-  if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)sb;
 }
 
 // e2m1 magnitudes 0 .. 6 have fp32 exponents 126 .. 129: the value at scale byte
