@@ -170,26 +170,25 @@ __device__ __forceinline__ void store_y(void* out, bool bf16, int64_t at, f32x4 
 }
 
 // silu(g) u on the hardware's exp2 and reciprocal (1 unit in the last place each): with
-// the argument's rounding h is within (8 + 2 |g|) 2^-24 of its value, before it is rounded
-// to 4 bits.  expf and a division took a quarter of a prompt's first product.
+// the argument's rounding h is within (8 + 2 |g|) 2^-24 of its value, and |g u| 2^-126
+// beyond that (a subnormal reciprocal is 0), before it is rounded to 4 bits.  expf and a division took a quarter of a prompt's first product.
 __device__ __forceinline__ float swiglu(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
 }
 
-// The sums of fragment m over the waves, SwiGLU and quantization of feature block
-// `block` of positions pos0 + 0 .. min(rows, 16) - 1: a position's 32 features are in the
+// The sums over the waves, SwiGLU and quantization of feature block `block` of positions pos0 + 0 .. min(rows, 16) - 1: a position's 32 features are in the
 // four lanes r + 16 q, eight each (4 q + 0..3 of both halves).
-template <int WAVES, int MF>
-__device__ __forceinline__ void experts_h(const ExpertsPlan& p, const f32x4 (&part)[WAVES][4 * MF][64], int m, int pos0,
-                                          int rows, int block) {
+template <int WAVES>
+__device__ __forceinline__ void experts_h(const ExpertsPlan& p, const f32x4 (&part)[WAVES][4][64], int pos0, int rows,
+                                          int block) {
   const int lane = threadIdx.x & 63, r = lane & 15;
   float v[8];
   f32x4 s[4];
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
-    s[a] = part[0][a * MF + m][lane];
+    s[a] = part[0][a][lane];
 #pragma unroll
-    for (int u = 1; u < WAVES; ++u) s[a] += part[u][a * MF + m][lane];
+    for (int u = 1; u < WAVES; ++u) s[a] += part[u][a][lane];
   }
   uint32_t top = 0;
 #pragma unroll
@@ -215,45 +214,38 @@ __device__ __forceinline__ void experts_h(const ExpertsPlan& p, const f32x4 (&pa
 }
 
 // First product, SwiGLU and quantization: a workgroup owns 32 features (their
-// gate and up rows: four fragments of 16) of one tile of up to 16 MF positions.
-template <int MF, int WAVES>
+// gate and up rows: four fragments of 16) of one tile of up to 16 positions.
+template <int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void experts_up_stream_kernel(ExpertsPlan p) {
-  __shared__ f32x4 part[WAVES][4 * MF][64];
+  __shared__ f32x4 part[WAVES][4][64];
   const int32_t* td = p.tiles + 3 * (int64_t)blockIdx.x;
   const int e = td[0], pos0 = td[1], rows = td[2];
   if (rows == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
   const int f0 = blockIdx.y * 32;
   const int nb = p.d / kMxBlock;
-  MxRow wrow[4], xrow[MF];
+  MxRow wrow[4];
 #pragma unroll
   for (int a = 0; a < 4; ++a) {   // gate features 0-15, 16-31, then up
     const int64_t row = (int64_t)e * 2 * p.f + (a >> 1) * p.f + f0 + 16 * (a & 1) + r;
     wrow[a] = {p.wgu + row * nb * kMxBlockBytes, p.wgu_scales + row * nb};
   }
+  const int64_t t = token_of(p, pair_at(p, pos0 + min(r, rows - 1)));
+  const MxRow xrow[1] = {{p.xq + t * nb * kMxBlockBytes, p.xs + t * nb}};
+  f32x4 acc[4][1];
 #pragma unroll
-  for (int m = 0; m < MF; ++m) {
-    const int64_t t = token_of(p, pair_at(p, pos0 + min(16 * m + r, rows - 1)));
-    xrow[m] = {p.xq + t * nb * kMxBlockBytes, p.xs + t * nb};
-  }
-  f32x4 acc[4][MF];
+  for (int a = 0; a < 4; ++a) acc[a][0] = f32x4{0, 0, 0, 0};
+  mx_stream<4, 1>(wrow, xrow, nb, wave, WAVES, acc);
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int m = 0; m < MF; ++m) acc[a][m] = f32x4{0, 0, 0, 0};
-  mx_stream<4, MF>(wrow, xrow, nb, wave, WAVES, acc);
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int m = 0; m < MF; ++m) part[wave][a * MF + m][lane] = acc[a][m];
+  for (int a = 0; a < 4; ++a) part[wave][a][lane] = acc[a][0];
   __syncthreads();
-  for (int m = wave; m < MF; m += WAVES) experts_h<WAVES, MF>(p, part, m, pos0 + 16 * m, rows - 16 * m, blockIdx.y);
+  if (wave == 0) experts_h<WAVES>(p, part, pos0, rows, blockIdx.y);
 }
 
 // Second product: 16 model features of one tile.
-template <int MF, int WAVES>
+template <int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void experts_down_stream_kernel(ExpertsPlan p) {
-  __shared__ f32x4 part[WAVES][MF][64];
+  __shared__ f32x4 part[WAVES][64];
   const int32_t* td = p.tiles + 3 * (int64_t)blockIdx.x;
   const int e = td[0], pos0 = td[1], rows = td[2];
   if (rows == 0) return;
@@ -262,28 +254,18 @@ __global__ __launch_bounds__(64 * WAVES) void experts_down_stream_kernel(Experts
   const int nb = p.f / kMxBlock;
   const int64_t wr = (int64_t)e * p.d + c0 + r;
   const MxRow wrow[1] = {{p.wd + wr * nb * kMxBlockBytes, p.wd_scales + wr * nb}};
-  MxRow hrow[MF];
-#pragma unroll
-  for (int m = 0; m < MF; ++m) {
-    const int64_t pos = pos0 + min(16 * m + r, rows - 1);
-    hrow[m] = {p.hq + pos * nb * kMxBlockBytes, p.hs + pos * nb};
-  }
-  f32x4 acc[1][MF];
-#pragma unroll
-  for (int m = 0; m < MF; ++m) acc[0][m] = f32x4{0, 0, 0, 0};
-  mx_stream<1, MF>(wrow, hrow, nb, wave, WAVES, acc);
-#pragma unroll
-  for (int m = 0; m < MF; ++m) part[wave][m][lane] = acc[0][m];
+  const int64_t pos = pos0 + min(r, rows - 1);
+  const MxRow hrow[1] = {{p.hq + pos * nb * kMxBlockBytes, p.hs + pos * nb}};
+  f32x4 acc[1][1] = {{f32x4{0, 0, 0, 0}}};
+  mx_stream<1, 1>(wrow, hrow, nb, wave, WAVES, acc);
+  part[wave][lane] = acc[0][0];
   __syncthreads();
-  for (int m = wave; m < MF; m += WAVES) {
-    f32x4 v = part[0][m][lane];
+  if (wave > 0 || r >= rows) return;
+  f32x4 v = part[0][lane];
 #pragma unroll
-    for (int u = 1; u < WAVES; ++u) v += part[u][m][lane];
-    if (16 * m + r < rows) {
-      const int64_t pair = pair_at(p, pos0 + 16 * m + r);
-      *reinterpret_cast<f32x4*>(p.ypair + pair * p.d + c0 + 4 * (lane >> 4)) = v;
-    }
-  }
+  for (int u = 1; u < WAVES; ++u) v += part[u][lane];
+  const int64_t pair = pair_at(p, pos0 + r);
+  *reinterpret_cast<f32x4*>(p.ypair + pair * p.d + c0 + 4 * (lane >> 4)) = v;
 }
 
 // ------------------------------------------------------------------ a few tokens
@@ -328,7 +310,7 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_few_kernel(ExpertsPlan 
   for (int a = 0; a < 4; ++a) part[wave][a][lane] = acc[a][0];
   __syncthreads();
   if (wave > 0) return;
-  experts_h<WAVES, 1>(p, part, 0, pair, 1, blockIdx.y);
+  experts_h<WAVES>(p, part, pair, 1, blockIdx.y);
 }
 
 // Second product and the sum over the token's pairs, in order: a wave per pair, as
@@ -565,18 +547,25 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(ExpertsPlan p, voi
 }
 
 // Positions of a tile of the plan, from the mean number of a routed slot's positions
-// (the load is not known on the host): how many rows of x a slot's weights meet.  The
-// largest tile has no registers for scale rows under 16 bytes (d or f under 512).
+// (the load is not known on the host): how many rows of x a slot's weights meet.  A
+// whole pass of d 2048, f 1408, 64 experts, 6 a token and 2 shared, us with tiles of
+// 16 | 128 | 256 positions, by that mean:
+//   4: 77 | 98 | 131     7: 86 | 101 | 132    12: 100 | 105 | 135   16: 126 | 116 | 145
+//   24: 170 | 122 | 152  48: 281 | 129 | 173  96: - | 143 | 180     160: - | 195 | 201
+//   192: - | 206 | 209   210: - | 234 | 223   281: - | 288 | 274    468: - | 417 | 387
+// The largest tile has no registers for scale rows under 16 bytes (d or f under 512).
 typedef MxTile<2, 4, 4, 2> Tile256;   // 256 rows of W by 256 positions, 8 waves
 typedef MxTile<2, 2, 2, 2> Tile128;
 int experts_tile_rows(int64_t n, int d, int f, int K, int E) {
   const int64_t mean = n * K / E;
   if (mean >= 192 && mx_words(d / kMxBlock) && mx_words(f / kMxBlock)) return 256;
-  return mean >= 48 ? 128 : mean >= 8 ? 64 : 16;
+  return mean >= 16 ? 128 : 16;
 }
 int experts_plan_blocks(int64_t pairs) { return (int)((pairs + kPlanPairs - 1) / kPlanPairs); }
 
-// Pairs up to which every pair reads its expert's weights itself.
+// Pairs up to which every pair reads its expert's weights itself: two launches instead of
+// four, against tiles of 16 positions in the block above, us by pairs:
+//   8: 15 | 22   16: 22 | 27   24: 29 | 31   32: 33 | 35   48: 46 | 40   96: 78 | 55
 constexpr int64_t kFewPairs = 32;
 
 namespace {
@@ -588,10 +577,9 @@ void run_tiles(const ExpertsPlan& p, bool bf16, hipStream_t s) {
   if (bf16) hipLaunchKernelGGL((experts_down_tile_kernel<T, DOWN, true>), down_grid, block, 0, s, p);
   else hipLaunchKernelGGL((experts_down_tile_kernel<T, DOWN, false>), down_grid, block, 0, s, p);
 }
-template <int MF, int WAVES>
 void run_stream(const ExpertsPlan& p, hipStream_t s) {
-  hipLaunchKernelGGL((experts_up_stream_kernel<MF, WAVES>), dim3(p.max_tiles, p.f / 32), dim3(64 * WAVES), 0, s, p);
-  hipLaunchKernelGGL((experts_down_stream_kernel<MF, WAVES>), dim3(p.max_tiles, p.d / 16), dim3(64 * WAVES), 0, s, p);
+  hipLaunchKernelGGL(experts_up_stream_kernel<4>, dim3(p.max_tiles, p.f / 32), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(experts_down_stream_kernel<4>, dim3(p.max_tiles, p.d / 16), dim3(256), 0, s, p);
 }
 }  // namespace
 
@@ -622,8 +610,7 @@ void launch_experts(const ExpertsPlan& p, const uint16_t* x, void* out, bool bf1
       else run_tiles<Tile128, false, false>(p, bf16, s);
       break;
     }
-    case 64: run_stream<4, 4>(p, s); break;
-    default: run_stream<1, 4>(p, s); break;
+    default: run_stream(p, s); break;
   }
   const bool short_pairs = bf16 && p.tile_rows >= 128;   // what the tiles stored
   const unsigned grid = (unsigned)(((int64_t)p.n * (p.d / (short_pairs ? 8 : 4)) + 255) / 256);

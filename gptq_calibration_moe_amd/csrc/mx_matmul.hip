@@ -11,25 +11,24 @@ __device__ __forceinline__ void mx_put(void* out, bool bf16, int64_t at, float v
   else static_cast<float*>(out)[at] = v;
 }
 
-// Few rows of a: a workgroup owns 16 rows of w and 16 MF rows of a; its waves
+// Few rows of a (at most 16 MF): a workgroup owns 16 rows of w and all of a; its waves
 // split the contraction and their sums are added in wave order (so results do
 // not depend on timing).
 template <int MF, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void mx_matmul_stream_kernel(const uint8_t* __restrict__ a,
                                                                       const uint8_t* __restrict__ as,
                                                                       const uint8_t* __restrict__ w,
-                                                                      const uint8_t* __restrict__ ws, int64_t m, int n,
+                                                                      const uint8_t* __restrict__ ws, int m, int n,
                                                                       int nb, void* __restrict__ out, bool bf16) {
   __shared__ f32x4 part[WAVES][MF][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
-  const int n0 = blockIdx.y * 16;
-  const int64_t m0 = (int64_t)blockIdx.x * 16 * MF;
+  const int n0 = blockIdx.x * 16;
   const int64_t wr = min(n0 + r, n - 1);   // rows past the end repeat the last one and are not stored
   const MxRow wrow[1] = {{w + wr * nb * kMxBlockBytes, ws + wr * nb}};
   MxRow arow[MF];
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
-    const int64_t ar = min(m0 + 16 * i + r, m - 1);
+    const int64_t ar = min(16 * i + r, m - 1);
     arow[i] = {a + ar * nb * kMxBlockBytes, as + ar * nb};
   }
   f32x4 acc[1][MF];
@@ -43,7 +42,7 @@ __global__ __launch_bounds__(64 * WAVES) void mx_matmul_stream_kernel(const uint
     f32x4 v = part[0][i][lane];
 #pragma unroll
     for (int u = 1; u < WAVES; ++u) v += part[u][i][lane];
-    const int64_t row = m0 + 16 * i + r;
+    const int64_t row = 16 * i + r;
     if (row >= m) continue;
     const int col = n0 + 4 * (lane >> 4);
 #pragma unroll
@@ -112,7 +111,7 @@ __global__ __launch_bounds__(T::kThreads) void mx_matmul_tile_kernel(const uint8
   const int wn0 = n0 + mx_wave_n<T>(wave) * T::FN * 32;
   mx_tile_products<T, WORDS>(W, X, [&](int r) { return min(r, nl); }, [&](int r) { return min(r, ml); }, nb,
                              wm0 < m && wn0 < n, MX_TILE_ARGS, acc);
-  mx_meet<0>();   // the buffers becomes the waves' output regions
+  mx_meet<0>();   // the buffers become the waves' output regions
   char* region = mx_region<T>(wave, MX_TILE_ARGS);
   if (bf16)
     mx_tile_rows16<T>(region, [&](int i, int j, uint2 (&h)[4]) { mx_pack_bf16(acc[i][j], h); },
@@ -146,20 +145,26 @@ void run_tiles(const MatmulCall& c, hipStream_t s) {
 typedef MxTile<2, 4, 4, 2> MxTile256;   // 256 x 256, 8 waves
 typedef MxTile<2, 2, 2, 2> MxTile128;   // 128 x 128, 4 waves
 
-// The larger tile moves half the bytes through LDS and L2 per product (m 65536, n 2816,
-// k 2048: 243 us against 290), once there are enough of them for most of the CUs
-// (176 tiles of 128, 44 of 256: 8.9 us against 15.8).  Odd scale rows (their fetch takes
-// registers that the larger tile does not have) stay with the smaller one.
+// Few rows of a go without LDS: they bring few bytes next to w, and a tile's stages take
+// longer than all of it.  In us, 16 rows of a at a time | 64 | tiles of 128:
+//   n 2816, k 2048:  m 8: 4.3 | 5.4 | 9.8    m 24: 5.8 | 5.9 | 10.0   m 64: 7.4 | 7.4 | 10.3
+//                    m 96: - | 10.9 | 11.2
+//   n 8192, k 4096:  m 8: 8.0 | 10.1 | 16.2  m 24: 14.3 | 12.0 | 16.5  m 64: 25.1 | 18.1 | 17.1
+//                    m 96: - | 31.8 | 18.8
+// The larger tile moves half the bytes through LDS and L2 per product, once there are
+// enough of them for most of the CUs; 128 | 256 rows a side, by the number of the larger:
+//   88: 14.5 | 20.0   128: 26.9 | 39.9   176: 24.5 | 22.1   256: 48.2 | 42.7   2816: 290 | 243
+// Odd scale rows (their fetch takes registers that the larger tile does not have) stay
+// with the smaller one.
 void launch_mx_matmul(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t m, int n, int k,
                       void* out, bool bf16, hipStream_t s) {
   const MatmulCall c{a, as, w, ws, m, n, k / kMxBlock, out, bf16};
   const unsigned nt = (unsigned)((n + 15) / 16);
   if (m <= 16)
-    hipLaunchKernelGGL((mx_matmul_stream_kernel<1, 8>), dim3(1, nt), dim3(512), 0, s, a, as, w, ws, m, n, c.nb, out, bf16);
-  else if (m <= 128)
-    hipLaunchKernelGGL((mx_matmul_stream_kernel<4, 4>), dim3((unsigned)((m + 63) / 64), nt), dim3(256), 0, s, a, as, w,
-                       ws, m, n, c.nb, out, bf16);
-  else if (mx_words(c.nb) && (m + 255) / 256 * ((n + 255) / 256) >= 192)
+    hipLaunchKernelGGL((mx_matmul_stream_kernel<1, 8>), dim3(nt), dim3(512), 0, s, a, as, w, ws, (int)m, n, c.nb, out, bf16);
+  else if (m <= 64)
+    hipLaunchKernelGGL((mx_matmul_stream_kernel<4, 4>), dim3(nt), dim3(256), 0, s, a, as, w, ws, (int)m, n, c.nb, out, bf16);
+  else if (mx_words(c.nb) && (m + 255) / 256 * ((n + 255) / 256) >= 160)
     run_tiles<MxTile256, true>(c, s);
   else if (mx_words(c.nb))
     run_tiles<MxTile128, true>(c, s);
