@@ -1277,7 +1277,6 @@ static size_t experts_layout(const clha_ctx* ctx, int64_t n, int f, void* ws, Ex
   p.xq = c.take<uint8_t>((size_t)n * d.d / 2);
   p.xs = c.take<uint8_t>((size_t)n * d.d / 32);
   p.blockcounts = c.take<int32_t>((size_t)clha::experts_plan_blocks(p.pairs) * p.E);
-  p.offsets = c.take<int32_t>((size_t)p.E);
   p.order = c.take<int32_t>((size_t)p.pairs);
   p.tiles = c.take<int32_t>((size_t)3 * p.max_tiles);
   p.hq = c.take<uint8_t>((size_t)all * f / 2);

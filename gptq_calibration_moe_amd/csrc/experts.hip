@@ -12,6 +12,8 @@
 // y_pair by pair, so a last kernel adds a token's pairs in a fixed order and no
 // result depends on timing.  A routed id outside 0 .. E-1 stands for no expert:
 // it is in no list and adds nothing.
+#include <algorithm>
+
 #include "kernels.h"
 #include "mx_stream.h"
 #include "mx_tile.h"
@@ -21,9 +23,12 @@ namespace clha {
 // ------------------------------------------------------------------ plan
 // Counting sort of the routed pairs by slot and the tiles: (slot, first position,
 // rows) with at most `rows` positions each.  Up to kPlanPairs pairs one workgroup does
-// all of it, beside the workgroups that quantize x in the same launch; beyond that
-// three launches with kPlanPairs pairs per workgroup.
+// all of it, beside the workgroups that quantize x in the same launch.  Beyond that
+// workgroups of that launch count a share of the pairs each, and a second launch of as
+// many places them, every one from all the counts: a scan in a launch of its own took
+// 9 us next to that.  At most kPlanBlocks shares keep those reads small.
 constexpr int kPlanPairs = 1024;
+constexpr int kPlanBlocks = 256;
 constexpr int kPlanThreads = 512;
 
 // The exclusive sum of v over the workgroup's threads; *total the whole.
@@ -47,24 +52,24 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* wave_sum, int3
   return base + x - v;
 }
 
-// Offsets and tiles of the slots, whose routed counts are in cnt[] (LDS): thread e
-// has slot e (slots <= kPlanThreads).  first[e] becomes the slot's first position.
-__device__ __forceinline__ void plan_tiles(const int32_t* cnt, int32_t* first, int32_t* wave_sum, int E, int slots,
-                                           int32_t n, int32_t pairs, int rows, int32_t* __restrict__ tiles,
-                                           int max_tiles) {
-  const int e = threadIdx.x;
-  const int32_t mine = e < E ? cnt[e] : e < slots ? n : 0;
+// Offsets of the slots, whose routed counts are in cnt[] (LDS), and in workgroup 0 the
+// tiles: thread e has slot e.  first[e] becomes the slot's first position.
+__device__ __forceinline__ void plan_tiles(const ExpertsPlan& p, const int32_t* cnt, int32_t* first, int32_t* wave_sum) {
+  const int e = threadIdx.x, rows = p.tile_rows;
+  const int32_t mine = e < p.E ? cnt[e] : e < p.E + p.shared ? p.n : 0;
   int32_t total;
-  const int32_t off = block_scan(e < E ? mine : 0, wave_sum, &total);
-  const int32_t pos = e < E ? off : pairs + (e - E) * n;
-  const int32_t tile0 = block_scan((mine + rows - 1) / rows, wave_sum, &total);
-  if (e < E) first[e] = pos;
-  for (int i = total + threadIdx.x; i < max_tiles; i += kPlanThreads) tiles[3 * (int64_t)i + 2] = 0;   // no tile
-  for (int i = 0; i * rows < mine; ++i) {
-    int32_t* d = tiles + 3 * (int64_t)(tile0 + i);
-    d[0] = e;
-    d[1] = pos + i * rows;
-    d[2] = min(rows, mine - i * rows);
+  const int32_t off = block_scan(e < p.E ? mine : 0, wave_sum, &total);
+  if (e < p.E) first[e] = off;
+  if (blockIdx.x == 0) {
+    const int32_t pos = e < p.E ? off : p.pairs + (e - p.E) * p.n;
+    const int32_t tile0 = block_scan((mine + rows - 1) / rows, wave_sum, &total);
+    for (int i = total + threadIdx.x; i < p.max_tiles; i += kPlanThreads) p.tiles[3 * (int64_t)i + 2] = 0;   // no tile
+    for (int i = 0; i * rows < mine; ++i) {
+      int32_t* d = p.tiles + 3 * (int64_t)(tile0 + i);
+      d[0] = e;
+      d[1] = pos + i * rows;
+      d[2] = min(rows, mine - i * rows);
+    }
   }
   __syncthreads();
 }
@@ -91,64 +96,58 @@ __device__ __forceinline__ void place_pairs(const int32_t* __restrict__ topk, in
   }
 }
 
-// Quantizes x (all of it, from the workgroups after the first) and, in workgroup 0,
-// makes the whole plan of at most kPlanPairs pairs.
-__global__ __launch_bounds__(kPlanThreads) void experts_begin_kernel(ExpertsPlan p, const uint16_t* __restrict__ x) {
+__device__ __forceinline__ int32_t share_of(const ExpertsPlan& p, int blocks) { return (p.pairs + blocks - 1) / blocks; }
+
+// The first `blocks` workgroups count their shares of the pairs (one alone makes the
+// whole plan), the others quantize x.
+__global__ __launch_bounds__(kPlanThreads) void experts_begin_kernel(ExpertsPlan p, const uint16_t* __restrict__ x,
+                                                                     int blocks) {
   __shared__ int32_t cnt[kMaxExperts], first[kMaxExperts], wave_sum[kPlanThreads / 64];
-  if (blockIdx.x > 0) {
-    const int64_t i = (int64_t)(blockIdx.x - 1) * kPlanThreads + threadIdx.x;
+  if ((int)blockIdx.x >= blocks) {
+    const int64_t i = (int64_t)(blockIdx.x - blocks) * kPlanThreads + threadIdx.x;
     if (i < (int64_t)p.n * (p.d / 8)) mx_quantize8(x + 8 * i, i, p.xq, p.xs);
     return;
   }
-  count_pairs(p.topk, 0, p.pairs, p.E, cnt);
-  plan_tiles(cnt, first, wave_sum, p.E, p.E + p.shared, p.n, p.pairs, p.tile_rows, p.tiles, p.max_tiles);
-  place_pairs(p.topk, 0, p.pairs, p.E, first, p.order);
+  const int64_t share = share_of(p, blocks), from = blockIdx.x * share, to = min(from + share, (int64_t)p.pairs);
+  count_pairs(p.topk, from, to, p.E, cnt);
+  if (blocks > 1) {
+    for (int e = threadIdx.x; e < p.E; e += kPlanThreads) p.blockcounts[(int64_t)blockIdx.x * p.E + e] = cnt[e];
+    return;
+  }
+  plan_tiles(p, cnt, first, wave_sum);
+  place_pairs(p.topk, from, to, p.E, first, p.order);
 }
 
-__global__ __launch_bounds__(kPlanThreads) void experts_count_kernel(ExpertsPlan p) {
-  __shared__ int32_t cnt[kMaxExperts];
-  const int64_t from = (int64_t)blockIdx.x * kPlanPairs;
-  count_pairs(p.topk, from, min(from + kPlanPairs, (int64_t)p.pairs), p.E, cnt);
-  for (int e = threadIdx.x; e < p.E; e += kPlanThreads) p.blockcounts[(int64_t)blockIdx.x * p.E + e] = cnt[e];
-}
-
-// One workgroup: each block's base within its slot (two threads per slot, each over
-// half of the blocks, eight counts loaded together), then offsets and tiles.
-__global__ __launch_bounds__(kPlanThreads) void experts_scan_kernel(ExpertsPlan p, int nblk) {
-  __shared__ int32_t cnt[kMaxExperts], first[kMaxExperts], wave_sum[kPlanThreads / 64];
+// Offsets and tiles from all the counts (two threads per slot, each over half of the
+// shares, eight counts loaded together); every workgroup places its share.
+__global__ __launch_bounds__(kPlanThreads) void experts_place_kernel(ExpertsPlan p, int blocks) {
+  __shared__ int32_t cnt[kMaxExperts], before[kMaxExperts], first[kMaxExperts], wave_sum[kPlanThreads / 64];
   const int e = threadIdx.x >> 1, part = threadIdx.x & 1;
-  const int lo = part * (nblk / 2), hi = part ? nblk : nblk / 2;
-  auto over = [&](int32_t run, bool write) {
+  const int lo = part * (blocks / 2), hi = part ? blocks : blocks / 2;
+  int32_t all = 0, mine = 0;   // of all shares, of those before this one
+  if (e < p.E)
     for (int b = lo; b < hi; b += 8) {
       int32_t c[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) c[j] = b + j < hi ? p.blockcounts[(int64_t)(b + j) * p.E + e] : 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (write && b + j < hi) p.blockcounts[(int64_t)(b + j) * p.E + e] = run;
-        run += c[j];
+        all += c[j];
+        mine += b + j < (int)blockIdx.x ? c[j] : 0;
       }
     }
-    return run;
-  };
-  const int32_t sum = e < p.E ? over(0, false) : 0;
-  const int32_t before = __shfl(sum, (threadIdx.x & 63) & ~1);   // of the first half
-  if (e < p.E) {
-    over(part ? before : 0, true);
-    if (part) cnt[e] = before + sum;
+  all += __shfl_xor(all, 1);
+  mine += __shfl_xor(mine, 1);
+  if (e < p.E && part == 0) {
+    cnt[e] = all;
+    before[e] = mine;
   }
   __syncthreads();
-  plan_tiles(cnt, first, wave_sum, p.E, p.E + p.shared, p.n, p.pairs, p.tile_rows, p.tiles, p.max_tiles);
-  for (int i = threadIdx.x; i < p.E; i += kPlanThreads) p.offsets[i] = first[i];
-}
-
-__global__ __launch_bounds__(kPlanThreads) void experts_scatter_kernel(ExpertsPlan p) {
-  __shared__ int32_t next[kMaxExperts];
-  for (int e = threadIdx.x; e < p.E; e += kPlanThreads)
-    next[e] = p.offsets[e] + p.blockcounts[(int64_t)blockIdx.x * p.E + e];
+  plan_tiles(p, cnt, first, wave_sum);
+  for (int i = threadIdx.x; i < p.E; i += kPlanThreads) first[i] += before[i];
   __syncthreads();
-  const int64_t from = (int64_t)blockIdx.x * kPlanPairs;
-  place_pairs(p.topk, from, min(from + kPlanPairs, (int64_t)p.pairs), p.E, next, p.order);
+  const int64_t share = share_of(p, blocks), from = blockIdx.x * share;
+  place_pairs(p.topk, from, min(from + share, (int64_t)p.pairs), p.E, first, p.order);
 }
 
 // ------------------------------------------------------------------ products
@@ -561,7 +560,9 @@ int experts_tile_rows(int64_t n, int d, int f, int K, int E) {
   if (mean >= 192 && mx_words(d / kMxBlock) && mx_words(f / kMxBlock)) return 256;
   return mean >= 16 ? 128 : 16;
 }
-int experts_plan_blocks(int64_t pairs) { return (int)((pairs + kPlanPairs - 1) / kPlanPairs); }
+int experts_plan_blocks(int64_t pairs) {
+  return (int)std::min<int64_t>((pairs + kPlanPairs - 1) / kPlanPairs, kPlanBlocks);
+}
 
 // Pairs up to which every pair reads its expert's weights itself: two launches instead of
 // four, against tiles of 16 positions in the block above, us by pairs:
@@ -590,16 +591,10 @@ void launch_experts(const ExpertsPlan& p, const uint16_t* x, void* out, bool bf1
     hipLaunchKernelGGL(experts_down_few_kernel<8>, dim3(p.n, p.d / 16), dim3(512), 0, s, p, out, bf16);
     return;
   }
-  if (p.pairs <= kPlanPairs) {
-    hipLaunchKernelGGL(experts_begin_kernel, dim3((unsigned)(1 + (chunks + kPlanThreads - 1) / kPlanThreads)),
-                       dim3(kPlanThreads), 0, s, p, x);
-  } else {
-    const int nblk = experts_plan_blocks(p.pairs);
-    launch_mx_quantize(x, true, p.n, p.d, p.d, p.xq, p.xs, s);
-    hipLaunchKernelGGL(experts_count_kernel, dim3(nblk), dim3(kPlanThreads), 0, s, p);
-    hipLaunchKernelGGL(experts_scan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p, nblk);
-    hipLaunchKernelGGL(experts_scatter_kernel, dim3(nblk), dim3(kPlanThreads), 0, s, p);
-  }
+  const int blocks = experts_plan_blocks(p.pairs);
+  hipLaunchKernelGGL(experts_begin_kernel, dim3((unsigned)(blocks + (chunks + kPlanThreads - 1) / kPlanThreads)),
+                     dim3(kPlanThreads), 0, s, p, x, blocks);
+  if (blocks > 1) hipLaunchKernelGGL(experts_place_kernel, dim3(blocks), dim3(kPlanThreads), 0, s, p, blocks);
   switch (p.tile_rows) {
     case 256: run_tiles<Tile256, true, true>(p, bf16, s); break;
     case 128: {

@@ -247,7 +247,6 @@ struct ExpertsPlan {
   // workspace
   uint8_t *xq, *xs;              // x in MXFP4: [n][d/2], [n][d/32]
   int32_t* blockcounts;          // [plan blocks][E]
-  int32_t* offsets;              // [E] first position of a routed slot
   int32_t* order;                // [pairs] pair at each position of the routed slots
   int32_t* tiles;                // [max_tiles][3] slot, first position, positions (0: no tile)
   uint8_t *hq, *hs;              // h in MXFP4 by position: [all pairs][f/2], [all pairs][f/32]

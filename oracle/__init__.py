@@ -572,13 +572,14 @@ def mx_values(codes, scales) -> np.ndarray:
     return np.where(s == 255, np.nan, v)
 
 
-def mx_experts(x, topk, weights, wgu, wd, n_routed: int, sum_eps: float = 0.0, pair_eps: float = 0.0):
+def mx_experts(x, topk, weights, wgu, wd, n_routed: int, sum_eps: float = 0.0, pair_eps: float = 0.0,
+               add_eps: float = 0.0):
     """The pass through MXFP4 experts in fp64; x fp64 [n, d], wgu fp64 [slots, 2f, d] and wd
     [slots, d, f] (values).  Returns (y, tol): tol bounds how far y may move when every product
     is summed with relative error sum_eps of its absolute sum and h is formed in fp32, including
     the codes of h that such an error can turn (h is rounded to 4 bits, so a value next to a
-    border may go either way), and when every pair's result is off by pair_eps of the largest
-    of its 32 columns."""
+    border may go either way), when every pair's result is off by pair_eps of the largest
+    of its 32 columns, and when adding a token's pairs is off by add_eps of their absolute sum."""
     x = mx_values(*mx_quantize(x))
     n, f, slots = x.shape[0], wd.shape[2], wd.shape[0]
     y, tol = np.zeros((n, wd.shape[1])), np.zeros((n, wd.shape[1]))
@@ -611,5 +612,6 @@ def mx_experts(x, topk, weights, wgu, wd, n_routed: int, sum_eps: float = 0.0, p
         if pair_eps:
             most = np.abs(pair).reshape(t.size, -1, 32).max(axis=2)
             tol[t] += np.abs(w[t, None]) * (pair_eps * np.repeat(most, 32, axis=1))
+        tol[t] += add_eps * np.abs(w[t, None] * pair)
         tol[t] += np.abs(w[t, None]) * (spread @ np.abs(wd[e]).T + sum_eps * (np.abs(q[0]) @ np.abs(wd[e]).T))
     return y, tol
