@@ -213,7 +213,8 @@ __device__ __forceinline__ void experts_h(const ExpertsPlan& p, const f32x4 (&pa
 }
 
 // First product, SwiGLU and quantization: a workgroup owns 32 features (their
-// gate and up rows: four fragments of 16) of one tile of up to 16 positions.
+// gate and up rows: four fragments of 16) of one tile of up to 16 positions.  Bound by
+// the weights: 48 tokens, 66 experts of d 2048, f 1408: 40 us for 202 MB, 5.0 TB/s.
 template <int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void experts_up_stream_kernel(ExpertsPlan p) {
   __shared__ f32x4 part[WAVES][4][64];
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(64 * WAVES) void experts_up_stream_kernel(ExpertsPl
   if (wave == 0) experts_h<WAVES>(p, part, pos0, rows, blockIdx.y);
 }
 
-// Second product: 16 model features of one tile.
+// Second product: 16 model features of one tile (the same 48 tokens: 21 us for 101 MB).
 template <int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void experts_down_stream_kernel(ExpertsPlan p) {
   __shared__ f32x4 part[WAVES][64];
@@ -269,7 +270,9 @@ __global__ __launch_bounds__(64 * WAVES) void experts_down_stream_kernel(Experts
 
 // ------------------------------------------------------------------ a few tokens
 // Without a plan: a workgroup per (pair, 32 features), then per (token, 16 model
-// features).  Every pair reads its expert's weights itself; h goes by pair.
+// features).  Every pair reads its expert's weights itself; h goes by pair.  One token, 8
+// experts of d 2048, f 1408: 15 us for both, 37 MB that would take 7.4 at a copy's rate;
+// half is two launches, each with a memory latency for its ids and one for its weights.
 
 __device__ __forceinline__ int slot_of(const ExpertsPlan& p, int32_t pair) {
   return pair < p.pairs ? p.topk[pair] : p.E + (pair - p.pairs) / p.n;
@@ -366,6 +369,9 @@ int64_t experts_tile_grid(int64_t max_tiles, int parts) {
 // First product: a wave's rows of W are FN/2 fragments of gate rows and the up rows
 // of the same features, so a lane holds both values of 16 features of a block of 32 and
 // its partner (lane ^ 32) the other 16: SwiGLU and quantization stay in registers.
+// 8192 tokens, 6 of 64 and 2 shared experts, d 2048, f 1408: 290 to 308 us for 756 GFLOP,
+// 2.5 PFLOP/s, of which the products are 250 to 270 (an eighth of the tiles are slots'
+// partial last ones) and SwiGLU and quantization the others.
 template <class T, bool WORDS>
 __global__ __launch_bounds__(T::kThreads) void experts_up_tile_kernel(ExpertsPlan p) {
   MX_TILE_LDS(T);
@@ -453,7 +459,9 @@ __device__ __forceinline__ float pair_value(int half, int field) {
   return field == 255 ? NAN : __builtin_ldexpf((float)half * (1.0f / 32767.0f), field - 126);
 }
 
-// Second product: rows stored by pair, in fp32 or (SHORT) as above.
+// Second product: rows stored by pair, in fp32 or (SHORT) as above.  The same 8192 tokens:
+// 228 to 240 us for 378 GFLOP, of which 147 to 160 are the products and the others the
+// output of 276 MB.
 template <class T, bool WORDS, bool SHORT>
 __global__ __launch_bounds__(T::kThreads) void experts_down_tile_kernel(ExpertsPlan p) {
   MX_TILE_LDS(T);
@@ -505,7 +513,8 @@ __global__ __launch_bounds__(T::kThreads) void experts_down_tile_kernel(ExpertsP
 }
 
 // y_t = sum of its pairs: the routed ones in order with their weights, then the
-// shared ones.  Four features per thread, or (SHORT) eight of bf16.
+// shared ones.  Four features per thread, or (SHORT) eight of bf16.  Bound by reading the
+// pair results: 60 us for 307 MB, 5.1 TB/s.
 template <bool SHORT>
 __global__ __launch_bounds__(256) void experts_combine_kernel(ExpertsPlan p, void* __restrict__ out, bool bf16) {
   constexpr int kCols = SHORT ? 8 : 4;

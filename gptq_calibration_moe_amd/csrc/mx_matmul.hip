@@ -11,9 +11,10 @@ __device__ __forceinline__ void mx_put(void* out, bool bf16, int64_t at, float v
   else static_cast<float*>(out)[at] = v;
 }
 
-// Few rows of a (at most 16 MF): a workgroup owns 16 rows of w and all of a; its waves
+// Few rows of a: a workgroup owns 16 rows of w and 16 MF rows of a; its waves
 // split the contraction and their sums are added in wave order (so results do
-// not depend on timing).
+// not depend on timing).  One row against 2816 x 2048: 4.0 us back to back, of which the
+// 3.1 MB would take 0.6: a launch, a memory latency and the waves' sum.
 template <int MF, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void mx_matmul_stream_kernel(const uint8_t* __restrict__ a,
                                                                       const uint8_t* __restrict__ as,
@@ -22,13 +23,13 @@ __global__ __launch_bounds__(64 * WAVES) void mx_matmul_stream_kernel(const uint
                                                                       int nb, void* __restrict__ out, bool bf16) {
   __shared__ f32x4 part[WAVES][MF][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.y * 16, m0 = blockIdx.x * 16 * MF;
   const int64_t wr = min(n0 + r, n - 1);   // rows past the end repeat the last one and are not stored
   const MxRow wrow[1] = {{w + wr * nb * kMxBlockBytes, ws + wr * nb}};
   MxRow arow[MF];
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
-    const int64_t ar = min(16 * i + r, m - 1);
+    const int64_t ar = min(m0 + 16 * i + r, m - 1);
     arow[i] = {a + ar * nb * kMxBlockBytes, as + ar * nb};
   }
   f32x4 acc[1][MF];
@@ -42,7 +43,7 @@ __global__ __launch_bounds__(64 * WAVES) void mx_matmul_stream_kernel(const uint
     f32x4 v = part[0][i][lane];
 #pragma unroll
     for (int u = 1; u < WAVES; ++u) v += part[u][i][lane];
-    const int64_t row = 16 * i + r;
+    const int64_t row = m0 + 16 * i + r;
     if (row >= m) continue;
     const int col = n0 + 4 * (lane >> 4);
 #pragma unroll
@@ -79,7 +80,10 @@ __device__ __forceinline__ void mx_put8(uint16_t* out, int64_t row, int64_t n, i
 // Many rows: one tile of mx_tile.h per workgroup.  Workgroup b runs on die
 // b % kXcds; a die takes a contiguous run of tiles, ordered in bands of 8 tiles
 // of rows of a, all columns per band, so the tiles it runs together share a few
-// panels of both operands in its L2.
+// panels of both operands in its L2.  m 65536, n 2816, k 2048 in bf16: 243 to 255 us, 3.0
+// to 3.1 PFLOP/s.  About 200 us are the products (their matrix instructions alone take 124
+// at the 6.1 PFLOP/s of random operands; with one workgroup a CU nothing fills the waits
+// at the stages' ends), the rest writes 369 MB of results.
 constexpr int kBand = 8;
 template <class T, bool WORDS>
 __global__ __launch_bounds__(T::kThreads) void mx_matmul_tile_kernel(const uint8_t* __restrict__ a,
@@ -146,11 +150,16 @@ typedef MxTile<2, 4, 4, 2> MxTile256;   // 256 x 256, 8 waves
 typedef MxTile<2, 2, 2, 2> MxTile128;   // 128 x 128, 4 waves
 
 // Few rows of a go without LDS: they bring few bytes next to w, and a tile's stages take
-// longer than all of it.  In us, 16 rows of a at a time | 64 | tiles of 128:
+// longer than all of it.  Every one of these workgroups reads its rows of a from L2, so
+// past two of them per CU that takes over.  In us, 16 rows of a workgroup | 64 | tiles of 128:
 //   n 2816, k 2048:  m 8: 4.3 | 5.4 | 9.8    m 24: 5.8 | 5.9 | 10.0   m 64: 7.4 | 7.4 | 10.3
-//                    m 96: - | 10.9 | 11.2
-//   n 8192, k 4096:  m 8: 8.0 | 10.1 | 16.2  m 24: 14.3 | 12.0 | 16.5  m 64: 25.1 | 18.1 | 17.1
-//                    m 96: - | 31.8 | 18.8
+//   n 8192, k 4096:  m 8: 8.0 | 10.1 | 16.2  m 24: 14.3 | 12.0 | 16.5  m 64: 25.1 | 17.7 | 17.0
+// and 64 | tiles by the workgroups' number, k 1440, 2048, 4096:
+//   352 (m 96, n 2816): 6.6 | 10.9, 10.8 | 11.1, 17.5 | 18.3
+//   512 (m 96, n 4096): 6.8 | 11.4, 10.9 | 11.1, 17.6 | 18.4
+//   512 (m 64, n 8192): 6.9 | 11.0, 11.0 | 10.5, 17.7 | 17.0
+//   704 (m 96, n 5632): 8.4 | 11.4, 14.7 | 11.3, 24.6 | 18.6
+//   1024 (m 96, n 8192): 10.7 | 11.5, 18.6 | 11.4, 31.7 | 18.7
 // The larger tile moves half the bytes through LDS and L2 per product, once there are
 // enough of them for most of the CUs; 128 | 256 rows a side, by the number of the larger:
 //   88: 14.5 | 20.0   128: 26.9 | 39.9   176: 24.5 | 22.1   256: 48.2 | 42.7   2816: 290 | 243
@@ -159,11 +168,13 @@ typedef MxTile<2, 2, 2, 2> MxTile128;   // 128 x 128, 4 waves
 void launch_mx_matmul(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t m, int n, int k,
                       void* out, bool bf16, hipStream_t s) {
   const MatmulCall c{a, as, w, ws, m, n, k / kMxBlock, out, bf16};
-  const unsigned nt = (unsigned)((n + 15) / 16);
+  const unsigned nt = (unsigned)((n + 15) / 16), mt = (unsigned)((m + 63) / 64);
   if (m <= 16)
-    hipLaunchKernelGGL((mx_matmul_stream_kernel<1, 8>), dim3(nt), dim3(512), 0, s, a, as, w, ws, (int)m, n, c.nb, out, bf16);
-  else if (m <= 64)
-    hipLaunchKernelGGL((mx_matmul_stream_kernel<4, 4>), dim3(nt), dim3(256), 0, s, a, as, w, ws, (int)m, n, c.nb, out, bf16);
+    hipLaunchKernelGGL((mx_matmul_stream_kernel<1, 8>), dim3(1, nt), dim3(512), 0, s, a, as, w, ws, (int)m, n, c.nb, out,
+                       bf16);
+  else if (m <= 128 && mt * nt <= 512)
+    hipLaunchKernelGGL((mx_matmul_stream_kernel<4, 4>), dim3(mt, nt), dim3(256), 0, s, a, as, w, ws, (int)m, n, c.nb, out,
+                       bf16);
   else if (mx_words(c.nb) && (m + 255) / 256 * ((n + 255) / 256) >= 160)
     run_tiles<MxTile256, true>(c, s);
   else if (mx_words(c.nb))

@@ -89,7 +89,9 @@ struct MxOperand {
 // base.  The buffers are separate arrays so that the compiler can tell a stage being
 // loaded from one being read.  WORDS: nb is a multiple of 4, at least 16.
 // acc[FN][FM] += the tile's products over nb blocks; a wave that is not active (none of
-// its rows exist) only takes part in the loading.
+// its rows exist) only takes part in the loading.  On return loads of the last stages may
+// still be on their way into the buffers: mx_meet<0>() before they are used for anything
+// else (the end of a program waits for its loads by itself).
 template <class T, bool WORDS, class WRow, class XRow>
 __device__ __forceinline__ void mx_tile_products(const MxOperand& W, const MxOperand& X, WRow&& wrow_of, XRow&& xrow_of,
                                                  int nb, bool active, char* b0, char* b1, uint4* sc,

@@ -421,6 +421,10 @@ __device__ __forceinline__ int route_quick(const float (&l)[V], const float (&b)
 }
 
 // BIAS: a bias is given; GROUPS: more than one group.
+// Memory is not the bound (4 E bytes a token): 65536 tokens of 64 experts, softmax, take
+// 12 us with the launch where 5.0 TB/s would take 4; 32749 tokens of 256 experts in groups
+// 40 against 7.  What is left are the rounds of the choice: each a maximum over 16 lanes
+// and its removal, one after the other.
 template <int V, bool BIAS, bool GROUPS, bool VEC>
 __global__ __launch_bounds__(256) void score_route_kernel(const float* __restrict__ logits,
                                                           const float* __restrict__ bias, int64_t n, int E, int K,

@@ -256,3 +256,8 @@ def test_products_beyond_one_launch_are_refused(ctx):
             n = min((1 << 36) // m, 524288)
             tiles = -(-m // tile) * -(-n // tile)
             assert (tiles + 7) // 8 * 8 * threads < 1 << 32
+
+
+@pytest.mark.parametrize("m,n,k", [(20, 8300, 96), (40, 8300, 512), (65, 4097, 160), (100, 8193, 512), (128, 4096, 544)])
+def test_few_rows_against_many_columns(ctx, m, n, k):
+    _check_matmul(ctx, np.random.default_rng(m + n + k), m, n, k)
