@@ -557,17 +557,21 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(ExpertsPlan p, voi
 // Positions of a tile of the plan, from the mean number of a routed slot's positions
 // (the load is not known on the host): how many rows of x a slot's weights meet.  A
 // whole pass of d 2048, f 1408, 64 experts, 6 a token and 2 shared, us with tiles of
-// 16 | 128 | 256 positions, by that mean:
-//   4: 77 | 98 | 131     7: 86 | 101 | 132    12: 100 | 105 | 135   16: 126 | 116 | 145
-//   24: 170 | 122 | 152  48: 281 | 129 | 173  96: - | 143 | 180     160: - | 195 | 201
-//   192: - | 206 | 209   210: - | 234 | 223   281: - | 288 | 274    468: - | 417 | 387
+// 16 | 32 | 64 | 128 | 256 positions, by that mean:
+//   4: 77 | 82 | - | 94 | 126         7: 87 | 87 | 94 | 101 | 131     12: 101 | 85 | - | 105 | 134
+//   24: 164 | 94 | 101 | 115 | 147    31: - | 103 | 103 | 119 | 153   40: - | 121 | 105 | 117 | 162
+//   48: - | 121 | 107 | 124 | 169     64: - | 147 | 124 | 126 | 170   79: - | 162 | 146 | 135 | -
+//   96: - | 182 | 148 | 137 | 176     144: - | 238 | 208 | 185 | 193
+//   192: - | 300 | - | 198 to 209 | 206 to 210    210: 234 | 223 (the last two)   281: 288 | 274   468: 417 | 387
 // The largest tile has no registers for scale rows under 16 bytes (d or f under 512).
 typedef MxTile<2, 4, 4, 2> Tile256;   // 256 rows of W by 256 positions, 8 waves
 typedef MxTile<2, 2, 2, 2> Tile128;
+typedef MxTile<2, 2, 2, 1> Tile64;    // 128 rows of W by 64 positions, 4 waves
+typedef MxTile<2, 1, 2, 1> Tile32;    // and by 32, 2 waves: three workgroups fit a CU
 int experts_tile_rows(int64_t n, int d, int f, int K, int E) {
   const int64_t mean = n * K / E;
   if (mean >= 192 && mx_words(d / kMxBlock) && mx_words(f / kMxBlock)) return 256;
-  return mean >= 16 ? 128 : 16;
+  return mean >= 72 ? 128 : mean >= 32 ? 64 : mean >= 6 ? 32 : 16;
 }
 int experts_plan_blocks(int64_t pairs) {
   return (int)std::min<int64_t>((pairs + kPlanPairs - 1) / kPlanPairs, kPlanBlocks);
@@ -586,6 +590,14 @@ void run_tiles(const ExpertsPlan& p, bool bf16, hipStream_t s) {
   hipLaunchKernelGGL((experts_up_tile_kernel<T, UP>), up_grid, block, 0, s, p);
   if (bf16) hipLaunchKernelGGL((experts_down_tile_kernel<T, DOWN, true>), down_grid, block, 0, s, p);
   else hipLaunchKernelGGL((experts_down_tile_kernel<T, DOWN, false>), down_grid, block, 0, s, p);
+}
+template <class T>
+void run_tiles(const ExpertsPlan& p, bool bf16, hipStream_t s) {
+  const bool up = mx_words(p.d / kMxBlock), down = mx_words(p.f / kMxBlock);
+  if (up && down) run_tiles<T, true, true>(p, bf16, s);
+  else if (up) run_tiles<T, true, false>(p, bf16, s);
+  else if (down) run_tiles<T, false, true>(p, bf16, s);
+  else run_tiles<T, false, false>(p, bf16, s);
 }
 void run_stream(const ExpertsPlan& p, hipStream_t s) {
   hipLaunchKernelGGL(experts_up_stream_kernel<4>, dim3(p.max_tiles, p.f / 32), dim3(256), 0, s, p);
@@ -606,17 +618,12 @@ void launch_experts(const ExpertsPlan& p, const uint16_t* x, void* out, bool bf1
   if (blocks > 1) hipLaunchKernelGGL(experts_place_kernel, dim3(blocks), dim3(kPlanThreads), 0, s, p, blocks);
   switch (p.tile_rows) {
     case 256: run_tiles<Tile256, true, true>(p, bf16, s); break;
-    case 128: {
-      const bool up = mx_words(p.d / kMxBlock), down = mx_words(p.f / kMxBlock);
-      if (up && down) run_tiles<Tile128, true, true>(p, bf16, s);
-      else if (up) run_tiles<Tile128, true, false>(p, bf16, s);
-      else if (down) run_tiles<Tile128, false, true>(p, bf16, s);
-      else run_tiles<Tile128, false, false>(p, bf16, s);
-      break;
-    }
+    case 128: run_tiles<Tile128>(p, bf16, s); break;
+    case 64: run_tiles<Tile64>(p, bf16, s); break;
+    case 32: run_tiles<Tile32>(p, bf16, s); break;
     default: run_stream(p, s); break;
   }
-  const bool short_pairs = bf16 && p.tile_rows >= 128;   // what the tiles stored
+  const bool short_pairs = bf16 && p.tile_rows >= 32;   // what the tiles stored
   const unsigned grid = (unsigned)(((int64_t)p.n * (p.d / (short_pairs ? 8 : 4)) + 255) / 256);
   if (short_pairs) hipLaunchKernelGGL(experts_combine_kernel<true>, dim3(grid), dim3(256), 0, s, p, out, bf16);
   else hipLaunchKernelGGL(experts_combine_kernel<false>, dim3(grid), dim3(256), 0, s, p, out, bf16);

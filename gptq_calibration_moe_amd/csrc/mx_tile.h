@@ -46,7 +46,8 @@ struct MxTile {
   static constexpr int TN = WN * FN * 32, TM = WM * FM * 32, kRows = TN + TM;
   static constexpr int kLoads = kRows / 8 / kWaves;        // load instructions of a wave per stage (8 rows each)
   static constexpr int kWLoads = TN / 8 / kWaves;          // the first of them, from W
-  static constexpr int kScaleRows = kRows / kThreads;      // rows of scales a thread fetches
+  static constexpr int kScaleSlots = (kRows + 63) / 64 * 64;   // rows of scales are fetched by whole waves
+  static constexpr int kScaleRows = (kScaleSlots + kThreads - 1) / kThreads;   // of a thread, at most
   static_assert(TN % (8 * kWaves) == 0 && TM % (8 * kWaves) == 0 && kWaves % 2 == 0, "each load instruction comes from one operand");
   static constexpr int kBufBytes = kRows * kStageBytes;
 };
@@ -61,7 +62,7 @@ __device__ __forceinline__ int mx_wave_m(int wave) { return wave / T::WN; }
 // LDS of a tile in a kernel: two stages' codes and two pairs of stages' scales.
 #define MX_TILE_LDS(T)                                                                     \
   __shared__ __attribute__((aligned(1024))) char mx_b0[T::kBufBytes], mx_b1[T::kBufBytes]; \
-  __shared__ uint4 mx_s[2 * T::kRows]
+  __shared__ uint4 mx_s[2 * T::kScaleSlots]
 
 #define MX_TILE_ARGS mx_b0, mx_b1, mx_s
 
@@ -85,8 +86,8 @@ struct MxOperand {
 };
 
 // wrow(r), xrow(r): the row, counted from the operand's base, of the tile's row r
-// (0 .. TN-1, 0 .. TM-1), always one that exists and less than 2^32 bytes from the
-// base.  The buffers are separate arrays so that the compiler can tell a stage being
+// (0 .. TN-1, 0 .. TM-1 and beyond), always one that exists and less than 2^32 bytes
+// from the base.  The buffers are separate arrays so that the compiler can tell a stage being
 // loaded from one being read.  WORDS: nb is a multiple of 4, at least 16.
 // acc[FN][FM] += the tile's products over nb blocks; a wave that is not active (none of
 // its rows exist) only takes part in the loading.  On return loads of the last stages may
@@ -108,8 +109,10 @@ __device__ __forceinline__ void mx_tile_products(const MxOperand& W, const MxOpe
     src[i] = (uint32_t)(i < T::kWLoads ? wrow_of(r) : xrow_of(r - T::TN)) * (uint32_t)(nb * kMxBlockBytes) +
              piece * kMxBlockBytes;
   }
-  // scale row i of this thread is tile row kThreads i + threadIdx.x (a wave's rows come from one operand)
-  static_assert(T::TN % 64 == 0 && T::kRows % T::kThreads == 0, "whole waves of scale rows");
+  // scale row i of this thread is tile row kThreads i + threadIdx.x (a wave's rows come from one operand;
+  // xrow_of takes rows past the tile's too, whose scales nothing reads)
+  static_assert(T::TN % 64 == 0, "a wave of scale rows of one operand");
+  auto has_scales = [&](int i) { return T::kThreads * (i + 1) <= T::kScaleSlots || T::kThreads * i + 64 * wave < T::kScaleSlots; };
   uint32_t ssrc[T::kScaleRows];
 #pragma unroll
   for (int i = 0; i < T::kScaleRows; ++i) {
@@ -137,7 +140,8 @@ __device__ __forceinline__ void mx_tile_products(const MxOperand& W, const MxOpe
 #pragma unroll
     for (int i = 0; i < T::kScaleRows; ++i) {
       const int r0 = T::kThreads * i + 64 * wave;
-      __builtin_amdgcn_global_load_lds((mx_glb_ptr)((r0 < T::TN ? ws : xs) + ssrc[i]), (mx_lds_ptr)(to + r0), 16, 0, 0);
+      if (has_scales(i))
+        __builtin_amdgcn_global_load_lds((mx_glb_ptr)((r0 < T::TN ? ws : xs) + ssrc[i]), (mx_lds_ptr)(to + r0), 16, 0, 0);
     }
   };
   auto first_word = [&](int s) {
@@ -168,7 +172,8 @@ __device__ __forceinline__ void mx_tile_products(const MxOperand& W, const MxOpe
   };
   auto store_scales = [&](uint4* to) {
 #pragma unroll
-    for (int i = 0; i < T::kScaleRows; ++i) to[T::kThreads * i + threadIdx.x] = sv[i];
+    for (int i = 0; i < T::kScaleRows; ++i)
+      if (has_scales(i)) to[T::kThreads * i + threadIdx.x] = sv[i];
   };
   // lane's first W and x rows in the tile, and its block slot of step 0
   const int r = lane & 31, g = lane >> 5;
@@ -259,11 +264,11 @@ __device__ __forceinline__ void mx_tile_products(const MxOperand& W, const MxOpe
   int s = 0, at = 0;   // the scales of stages s and s + 1 are at sc + at
 #pragma unroll 1
   for (; s + 2 <= full; s += 2) {
-    turn(s, b0, b1, sc + at, sc + (T::kRows - at), J0);
-    turn(s + 1, b1, b0, sc + at, sc + (T::kRows - at), J1);
-    at = T::kRows - at;
+    turn(s, b0, b1, sc + at, sc + (T::kScaleSlots - at), J0);
+    turn(s + 1, b1, b0, sc + at, sc + (T::kScaleSlots - at), J1);
+    at = T::kScaleSlots - at;
   }
-  if (s < full) turn(s, b0, b1, sc + at, sc + (T::kRows - at), J0);
+  if (s < full) turn(s, b0, b1, sc + at, sc + (T::kScaleSlots - at), J0);
   if (full < stages) {   // blocks left .. 7 of the last stage are past the end
     const int half = full & 1, left = nb - full * kStageBlocks;
     mx_meet<0>();

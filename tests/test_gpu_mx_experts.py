@@ -252,3 +252,19 @@ def test_more_pairs_than_one_share_of_the_plan_each(dtype):
     many = b.run(x.repeat(100, 1), np.tile(topk, (100, 1)), np.tile(w, (100, 1)), dtype=dtype).view(100, 500, 128)
     b.check(many[0], x, topk, w)
     assert torch.equal(many, many[:1].expand_as(many))
+
+
+# mean positions of a slot from 6 to 192 and beyond: every tile, with scale rows of whole words
+# (d, f from 512) and without, contractions that end inside a stage
+TILES = [(512, 512, 8, 2, 1, 60), (640, 128, 5, 1, 0, 33), (128, 640, 6, 3, 0, 40), (384, 384, 4, 2, 2, 50),
+         (512, 640, 4, 2, 1, 80), (640, 128, 3, 1, 1, 150), (128, 512, 4, 4, 0, 60), (256, 384, 5, 2, 0, 160),
+         (1408, 512, 4, 2, 0, 200), (512, 128, 4, 2, 1, 300), (128, 512, 2, 1, 0, 200), (896, 640, 3, 2, 1, 350)]
+
+
+@pytest.mark.parametrize("d,f,E,K,shared,n", TILES)
+def test_every_tile_matches_oracle(d, f, E, K, shared, n):
+    b = Block(d + f + E + n + 1, d, f, E, K, shared, n)
+    x, topk, w = b.tokens(n)
+    topk[1::9, 0] = -1
+    b.check(b.run(x, topk, w, dtype=torch.float32), x, topk, w)
+    b.check(b.run(x, topk, w), x, topk, w)
