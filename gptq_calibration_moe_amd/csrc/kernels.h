@@ -233,7 +233,9 @@ void launch_mx_matmul(const uint8_t* a, const uint8_t* as, const uint8_t* w, con
 constexpr int kMaxShared = 256;                            // shared experts of one pass
 constexpr int kMaxExpertSlots = kMaxExperts + kMaxShared;  // routed and shared experts
 constexpr int64_t kMaxExpertPairs = (int64_t)1 << 27;      // (token, expert) pairs of one pass
-// pairs x the wider of d and f, for the same reason: (pairs/128 + 544) (f/64) 256 threads.
+// pairs x the wider of d and f, for the same reason: (pairs/128 + 544) (f/64) 256 threads
+// (tiles of fewer positions have more, but are taken for at most 72 kMaxExperts tokens,
+// whose pairs x f stay below 2^35.3: (pairs/64 + 544) (f/64) 256).
 constexpr int64_t kMaxExpertWork = (int64_t)1 << 36;
 constexpr int64_t kMaxExpertValues = (int64_t)1 << 33;     // values of x of one pass: its codes stay within 32-bit offsets
 struct ExpertsPlan {
